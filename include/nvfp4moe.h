@@ -288,6 +288,41 @@ int moe_expert_ffn_nvfp4(const nvfp4_moe_args *args, void *ws, size_t ws_bytes, 
 int moe_expert_ffn_nvfp4_noalloc(const nvfp4_moe_args *args, void *stream);
 
 /*
+ * moe_route -- the router's decision for T tokens: the k expert ids and
+ * weights per token that moe_expert_ffn_nvfp4 takes (topk_ids, topk_w), from
+ * the router's logits.
+ *   logits  [T][E], bf16 (logits_dtype 0) or fp32 (1).  A NaN or -inf logit
+ *           masks that expert for that token; +inf counts as the largest
+ *           finite value.
+ *   scoring 0: softmax over the token's experts that are not masked;
+ *           1: sigmoid of each logit
+ *   bias    nullable fp32 [E]: added to the scores for the choice only, not
+ *           for the weights.  NaN or -inf switches an expert off.
+ *   n_group, topk_group, group_top: experts in n_group groups of E / n_group
+ *           consecutive ones, of which a token uses the topk_group best; a
+ *           group's value is the sum of its group_top (1 or 2) largest
+ *           choice values (score, plus bias).  1, 1, 1: no groups.
+ *   ids     int32 [T][k]: the k best choices of the groups in use, best
+ *           first.  The order is that of the exact values (where fp32 could
+ *           not tell two apart, fp64 decides); ties go to the lowest index,
+ *           for experts and for groups.  With fewer than k experts to choose
+ *           from the remaining ids are -1, which moe_expert_ffn_nvfp4 skips.
+ *   weights fp32 [T][k]: scale * score, or with renormalize 1 scale * score /
+ *           (sum of the token's chosen scores); 0 where the id is -1
+ *   n_tokens nullable, device int32: only the first *n_tokens tokens are
+ *           routed; the rows behind them get id -1 and weight 0 (a padded
+ *           batch, also in a captured graph)
+ * Requirements: T >= 0, 1 <= E <= 512, 1 <= k <= 32 (else
+ * NVFP4_ERR_UNSUPPORTED above those), n_group divides E and is at most 64,
+ * 1 <= topk_group <= n_group, k <= topk_group * (E / n_group), T * k <= 2^30;
+ * logits aligned to 16 bytes.  No workspace; ids and weights must not overlap
+ * the logits.
+ */
+int moe_route(const void *logits, int logits_dtype, int64_t T, int64_t E, int64_t k, int scoring, const float *bias,
+              int64_t n_group, int64_t topk_group, int group_top, int renormalize, float scale,
+              const int32_t *n_tokens, int32_t *ids, float *weights, void *stream);
+
+/*
  * MXFP4 -- a separately labelled format, NOT the pages' NVFP4: the Open
  * Compute Project "Microscaling Formats (MX) Specification" v1.0 format
  * that gfx950's scaled FP4 MFMA (v_mfma_scale_f32_32x32x64_f8f6f4) consumes,

@@ -6,6 +6,7 @@ device memory (``data_ptr()``) and the current stream; nothing here computes
 on the host.  If the shared library has not been built this module raises on
 import -- there is no fallback path.
 """
+import contextlib
 import ctypes
 import os
 
@@ -64,6 +65,8 @@ _SIG = {
     "mxfp4_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i64, ctypes.c_int, _vp, _vp]),
     "mxfp4_linear_workspace_size": (_sz, [_i64, _i64, _i64]),
     "mxfp4_linear": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _i64, ctypes.c_int, _vp, _vp, _sz, _vp]),
+    "moe_route": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _i64, ctypes.c_int,
+                                 ctypes.c_int, ctypes.c_float, _vp, _vp, _vp, _vp]),
     "moe_expert_ffn_nvfp4_workspace_size": (_sz, [ctypes.POINTER(MoeArgs)]),
     "moe_expert_ffn_nvfp4": (ctypes.c_int, [ctypes.POINTER(MoeArgs), _vp, _sz, _vp]),
     "moe_expert_ffn_nvfp4_noalloc": (ctypes.c_int, [ctypes.POINTER(MoeArgs), _vp]),
@@ -262,6 +265,65 @@ def mx_linear_workspace(M, K, N, device):
     """A dedicated workspace for mxfp4_linear (e.g. for graph capture)."""
     return torch.empty(max(int(_lib.mxfp4_linear_workspace_size(M, K, N)), 256), dtype=torch.uint8,
                        device=device)
+
+
+# ------------------------------------------------------------------ router
+def _on(device, *tensors):
+    """The device to launch on (a context manager): that of the call's tensors,
+    all of which must be there."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors of a call must be on one device, got {device} and {t.device}")
+    return torch.cuda.device(device) if torch.cuda.current_device() != device.index else contextlib.nullcontext()
+
+
+_SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def route(logits, topk, scoring="softmax", bias=None, n_group=1, topk_group=1, group_top=1, renormalize=True,
+          scale=1.0, n_tokens=None, out=None):
+    """Routing of tokens to experts: logits [T][E] (bf16 or float32) -> (ids
+    int32 [T][topk], weights float32 [T][topk]), as moe_expert_ffn takes them.
+
+    scoring: "softmax" (over the token's experts) or "sigmoid".  bias: float32
+    [E], added to the scores for the choice only.  n_group, topk_group,
+    group_top: the experts in n_group groups of consecutive ones, of which a
+    token uses the topk_group with the largest sum of their group_top (1 or
+    2) best choices.  renormalize: divide the chosen scores by their sum;
+    scale: factor on the weights.  A NaN or -inf logit (or bias) masks an
+    expert; where too few are left, ids are -1 and weights 0, which
+    moe_expert_ffn skips.  Experts come best first, ties by the lowest index.
+    n_tokens: int32 [1] on the device; rows behind it get id -1, weight 0.
+    out: (ids, weights) to fill."""
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    _require(logits, logits.dtype, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T][E]")
+    T, E = logits.shape
+    if scoring not in _SCORING:
+        raise ValueError(f"scoring must be one of {sorted(_SCORING)}, got {scoring!r}")
+    _require(bias, torch.float32, "bias")
+    if bias is not None and bias.shape != (E,):
+        raise ValueError(f"bias must be [{E}], got {tuple(bias.shape)}")
+    _require(n_tokens, torch.int32, "n_tokens")
+    if n_tokens is not None and n_tokens.numel() != 1:
+        raise ValueError("n_tokens must hold one value")
+    dev = logits.device
+    if out is None:
+        ids = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, max(topk, 0)), dtype=torch.float32, device=dev)
+    else:
+        ids, weights = out
+        for t, d, n in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
+            _require(t, d, n)
+            if t.shape != (T, topk):
+                raise ValueError(f"{n} must be [{T}][{topk}], got {tuple(t.shape)}")
+    with _on(dev, bias, n_tokens, ids, weights):
+        _check(_lib.moe_route(_p(logits), 0 if logits.dtype == torch.bfloat16 else 1, T, E, topk, _SCORING[scoring],
+                              _p(bias), n_group, topk_group, group_top, int(bool(renormalize)), scale, _p(n_tokens),
+                              _p(ids), _p(weights), _stream(dev)), "moe_route")
+    return ids, weights
 
 
 def pair_scales(sf, out=None):

@@ -267,6 +267,38 @@ int nvfp4_linear(const uint16_t* x, int64_t M, int64_t K, const float* x_gs_in, 
                     "nvfp4_linear");
 }
 
+// ------------------------------------------------------------------ router
+int moe_route(const void* logits, int logits_dtype, int64_t T, int64_t E, int64_t k, int scoring, const float* bias,
+              int64_t n_group, int64_t topk_group, int group_top, int renormalize, float scale,
+              const int32_t* n_tokens, int32_t* ids, float* weights, void* stream) {
+  g_last_error[0] = 0;
+  if (T < 0 || E < 1 || k < 1) return fail(NVFP4_ERR_INVALID_ARG, "moe_route: need T >= 0, E >= 1 and k >= 1");
+  if (logits_dtype != 0 && logits_dtype != 1)
+    return fail(NVFP4_ERR_INVALID_ARG, "moe_route: logits_dtype must be 0 (bf16) or 1 (fp32)");
+  if (scoring != 0 && scoring != 1)
+    return fail(NVFP4_ERR_INVALID_ARG, "moe_route: scoring must be 0 (softmax) or 1 (sigmoid)");
+  if (renormalize != 0 && renormalize != 1) return fail(NVFP4_ERR_INVALID_ARG, "moe_route: renormalize must be 0 or 1");
+  if (E > 512 || k > 32) return fail(NVFP4_ERR_UNSUPPORTED, "moe_route: need E <= 512 and k <= 32");
+  if (n_group < 1 || E % n_group != 0 || topk_group < 1 || topk_group > n_group)
+    return fail(NVFP4_ERR_INVALID_ARG,
+                "moe_route: n_group must divide E and topk_group be 1 .. n_group (E=%lld n_group=%lld topk_group=%lld)",
+                (long long)E, (long long)n_group, (long long)topk_group);
+  if (n_group > 64) return fail(NVFP4_ERR_UNSUPPORTED, "moe_route: need n_group <= 64");
+  if (group_top != 1 && group_top != 2) return fail(NVFP4_ERR_INVALID_ARG, "moe_route: group_top must be 1 or 2");
+  if (k > topk_group * (E / n_group))
+    return fail(NVFP4_ERR_INVALID_ARG, "moe_route: k %lld exceeds the %lld experts of topk_group groups", (long long)k,
+                (long long)(topk_group * (E / n_group)));
+  if (T > ((int64_t)1 << 30) / k) return fail(NVFP4_ERR_UNSUPPORTED, "moe_route: too many (token, expert) pairs");
+  if (T == 0) return NVFP4_OK;
+  if (!logits || !ids || !weights) return fail(NVFP4_ERR_INVALID_ARG, "moe_route: null pointer");
+  if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(n_tokens, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "moe_route: misaligned pointer (logits need 16 bytes)");
+  return hip_status(nvfp4::launch_moe_route(logits, logits_dtype == 0, T, (int)E, bias, scoring == 1, (int)k,
+                                            (int)n_group, (int)topk_group, group_top, renormalize == 1, scale,
+                                            n_tokens, ids, weights, reinterpret_cast<hipStream_t>(stream)),
+                    "moe_route");
+}
+
 // ------------------------------------------------------------------ MXFP4
 // The separately labelled OCP MX v1.0 format (E8M0 scale per 32 elements)
 // on gfx950's scaled FP4 MFMA.

@@ -133,6 +133,13 @@ hipError_t launch_combine(const float* o, const int32_t* ids, int E, int64_t T, 
                           bool bf16_out, void* out, hipStream_t s, const uint16_t* o_f16 = nullptr,
                           const int8_t* o_exp = nullptr);
 
+// ---- router.hip
+// Expert ids and weights of T tokens from logits [T][E] (moe_route); n_group
+// divides E and is at most 64, E <= 512, k <= 32.
+hipError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, const float* bias, bool sigmoid, int k,
+                            int n_group, int topk_group, int group_top, bool renormalize, float scale,
+                            const int32_t* n_tokens, int32_t* ids, float* w, hipStream_t s);
+
 // ---- mxfp4.hip (OCP MX v1.0 MXFP4: E8M0 scale per 32 elements, E2M1 elements)
 // n bf16 values (n % 32 == 0) -> q [n/2] (element 2i in the low nibble of
 // byte i), sc [n/32] E8M0 codes

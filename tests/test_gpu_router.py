@@ -1,0 +1,239 @@
+"""Routing of tokens to experts on the GPU against its definition in 64 bits:
+the ids are equal, the weights within the tolerance that weight_tolerance derives."""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from gpu_util import dev_bf16, dev_f32, host
+from router_util import route_rows, weight_tolerance
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module")
+def nv():
+    import quantization_nvfp4_quantize_amd as nv
+    return nv
+
+
+def _check(nv, logits, k, bias=None, scale=1.0, **kw):
+    ids, w = nv.route(logits, k, bias=bias, scale=scale, **kw)
+    z = host(logits.double())
+    want, ww = route_rows(z, k, bias=None if bias is None else host(bias.double()), scale=scale, **kw)
+    got, gw = host(ids), host(w).astype(np.float64)
+    bad = np.argwhere((got != want).any(1)).ravel()
+    assert bad.size == 0, (bad[:5], got[bad[:3]], want[bad[:3]])
+    off = np.abs(gw - ww) - weight_tolerance(z, want, ww, scale)
+    assert (off <= 0).all(), (off.max(), gw.ravel()[off.argmax()], ww.ravel()[off.argmax()])
+    assert (gw[want < 0] == 0).all()
+    return ids, w
+
+
+def _logits(T, E, seed, dtype=torch.float32, std=1.5):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(T, E, generator=g) * std).to(dtype).to(DEV)
+
+
+def _bias(E, seed):
+    g = torch.Generator().manual_seed(seed + 1000)
+    return (torch.round(torch.randn(E, generator=g) * 20) * 0.001).to(DEV)
+
+
+# (T, E, k, n_group, topk_group, group_top): one lane with one expert up to
+# eight (and fifteen: 33 groups of 15 on one lane each), lanes that are not
+# filled, experts that do not divide over the lanes
+SHAPES = [(1, 1, 1, 1, 1, 1), (3, 2, 2, 1, 1, 1), (5, 8, 2, 1, 1, 1), (1, 256, 8, 1, 1, 1), (7, 63, 4, 1, 1, 1),
+          (9, 64, 32, 1, 1, 1), (4, 65, 6, 1, 1, 1), (130, 256, 8, 8, 4, 2), (6, 160, 6, 8, 3, 1),
+          (6, 160, 6, 8, 3, 2), (5, 384, 8, 1, 1, 1), (3, 511, 10, 1, 1, 1), (17, 512, 32, 16, 16, 2),
+          (4, 495, 12, 33, 20, 2), (4, 128, 2, 64, 1, 2), (5, 12, 3, 3, 2, 2), (2, 510, 9, 51, 7, 1),
+          (3, 9, 9, 9, 9, 2), (66, 72, 6, 1, 1, 1)]
+
+
+@pytest.mark.parametrize("T,E,k,n_group,topk_group,group_top", SHAPES)
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_shapes(nv, T, E, k, n_group, topk_group, group_top, scoring, dtype):
+    z = _logits(T, E, T * 7 + E + k, dtype)
+    for bias in (None, _bias(E, E)):
+        for renorm in (True, False):
+            _check(nv, z, k, bias=bias, scoring=scoring, n_group=n_group, topk_group=topk_group,
+                   group_top=group_top, renormalize=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("groups", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
+def test_route_masks_and_extremes(nv, scoring, with_bias, groups):
+    E = 32
+    z = _logits(16, E, 5)
+    lowest = torch.finfo(torch.float32).min
+    z[0] = -INF                      # nothing left
+    z[1] = NAN                       # nothing left
+    z[2] = -INF
+    z[2, 17] = -3.0                  # one expert left, fewer than k
+    z[3, ::2] = NAN                  # half of them
+    z[4] = lowest                    # the lowest value is a value, not a mask
+    z[5, :24] = lowest
+    z[6, 3] = z[6, 30] = INF         # counts as the largest finite value, twice: they tie
+    z[7] = 0.0
+    z[7, 1::2] = -0.0                # equal to zero: ties by index
+    z[8] = 1.25                      # all equal
+    z[9, :8] = -INF                  # a group without a live expert
+    z[10] = -200.0                   # scores that vanish in fp32
+    z[10, 5] = -199.0
+    z[11, :] = torch.linspace(-120, 80, E)
+    z[12] = -INF
+    z[12, 8:11] = torch.tensor([1.0, 2.0, 3.0])
+    z[13, 0] = torch.finfo(torch.float32).max
+    z[14] = 1e-40                    # below the normal range
+    z[14, 9] = 2e-40
+    bias = _bias(E, 3) if with_bias else None
+    for renorm in (True, False):
+        _check(nv, z, 6, bias=bias, scoring=scoring, n_group=groups[0], topk_group=groups[1], group_top=groups[2],
+               renormalize=renorm)
+        _check(nv, z.bfloat16(), 6, bias=bias, scoring=scoring, n_group=groups[0], topk_group=groups[1],
+               group_top=groups[2], renormalize=renorm)
+
+
+def test_route_bias_switches_experts_off_and_on(nv):
+    z = _logits(20, 48, 9)
+    b = _bias(48, 9)
+    b[3], b[20], b[21] = NAN, -INF, -INF
+    b[40], b[7] = INF, INF           # always first, by index
+    ids, _ = _check(nv, z, 5, bias=b, scoring="sigmoid")
+    assert not np.isin(host(ids), [3, 20, 21]).any()
+    assert (host(ids)[:, :2] == [7, 40]).all()
+    b = torch.full((48,), -INF, device=DEV)
+    b[11] = 0.5
+    ids, w = _check(nv, z, 5, bias=b, scoring="softmax")
+    assert (host(ids)[:, 1:] == -1).all() and (host(w)[:, 1:] == 0).all()
+    b[:] = 1e30                      # a bias that swallows every score: fp64 does not separate them either
+    ids, _ = nv.route(z, 5, bias=b)
+    assert (host(ids) == np.arange(5)).all()
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [(1, 1, 1), (8, 4, 2)])
+def test_route_decides_between_neighbours(nv, scoring, groups):
+    """Choices that lie closer together than fp32 scores are exact."""
+    E, T = 64, 64
+    z = _logits(T, E, 21, std=0.5)
+    zz = z.double()
+    s = torch.softmax(zz, 1) if scoring == "softmax" else torch.sigmoid(zz)
+    # one bias vector per row: every expert's choice lands next to 0.75, the
+    # rounding of the bias to fp32 decides
+    for t in range(T):
+        b = (0.75 - s[t]).float()
+        _check(nv, z[t:t + 1], 8, bias=b, scoring=scoring, n_group=groups[0], topk_group=groups[1],
+               group_top=groups[2])
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_decides_between_neighbouring_groups(nv, scoring):
+    """Groups whose sums differ below fp32's resolution, without a bias."""
+    E, G = 64, 8
+    z = _logits(G, E, 33)
+    for t in range(G):
+        g = torch.Generator().manual_seed(t)
+        base = torch.randn(E // G, generator=g)
+        for j in range(G):           # the same values in another order, one of them a step away
+            v = base[torch.randperm(E // G, generator=g)].clone()
+            v[v.argmax()] = torch.nextafter(v.max(), torch.tensor(INF if j % 3 else -INF))
+            z[t, j * (E // G):(j + 1) * (E // G)] = v.to(DEV)
+    _check(nv, z, 8, scoring=scoring, n_group=G, topk_group=4, group_top=2)
+
+
+def test_route_large_batch(nv):
+    """Many tokens, against torch in 64 bits (values without ties)."""
+    T, E, k = 40001, 256, 8
+    z = _logits(T, E, 2)
+    b = _bias(E, 2)
+    ids, w = nv.route(z, k, scoring="sigmoid", bias=b)
+    s = torch.sigmoid(z.double())
+    c, want = torch.sort(s + b.double(), dim=1, descending=True, stable=True)
+    assert torch.equal(ids.long(), want[:, :k])
+    part = s.gather(1, want[:, :k])
+    part = part / part.sum(1, keepdim=True)
+    assert float((w - part).abs().max()) <= 40 * 2.0 ** -24
+
+
+def test_route_padded_batch_and_out(nv):
+    T, E, k = 37, 96, 4
+    z = _logits(T, E, 4)
+    ids0, w0 = nv.route(z, k)
+    for n in (0, 1, 36, 37, 50, -3):
+        out = (torch.full((T, k), 77, dtype=torch.int32, device=DEV), torch.full((T, k), 7.0, device=DEV))
+        ids, w = nv.route(z, k, n_tokens=torch.tensor([n], dtype=torch.int32, device=DEV), out=out)
+        assert ids is out[0] and w is out[1]
+        m = max(0, min(n, T))
+        assert torch.equal(ids[:m], ids0[:m]) and torch.equal(w[:m], w0[:m])
+        assert (ids[m:] == -1).all() and (w[m:] == 0).all()
+
+
+def test_route_graph_and_streams(nv):
+    """A captured call follows its inputs over replays, with eager calls on
+    the same stream and another one in between."""
+    T, E, k = 50, 160, 6
+    z, b = _logits(T, E, 6), _bias(E, 6)
+    n = torch.tensor([T], dtype=torch.int32, device=DEV)
+    kw = dict(scoring="sigmoid", bias=b, n_group=8, topk_group=3, group_top=2, n_tokens=n)
+    nv.route(z, k, **kw)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ids, w = nv.route(z, k, **kw)
+    side = torch.cuda.Stream()
+    for i in range(4):
+        z.copy_(_logits(T, E, 60 + i))
+        n.fill_(T - 11 * i)
+        g.replay()
+        eager = nv.route(z, k, **kw)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            other = nv.route(z, k, **kw)
+        torch.cuda.synchronize()
+        for a in (eager, other):
+            assert torch.equal(a[0], ids) and torch.equal(a[1], w), i
+
+
+def test_route_refuses_bad_tensors(nv):
+    z = _logits(8, 32, 1)
+    for bad in (dict(bias=torch.zeros(31, device=DEV)), dict(bias=torch.zeros(32, device=DEV).bfloat16()),
+                dict(scoring="tanh"), dict(n_tokens=torch.zeros(2, dtype=torch.int32, device=DEV)),
+                dict(n_tokens=torch.zeros(1, dtype=torch.int32)),
+                dict(out=(torch.zeros(8, 3, dtype=torch.int32, device=DEV), torch.zeros(8, 4, device=DEV)))):
+        with pytest.raises(ValueError):
+            nv.route(z, 4, **bad)
+    with pytest.raises(ValueError, match="contiguous"):
+        nv.route(z[:, ::2], 4)
+    with pytest.raises(nv.Nvfp4Error):
+        nv.route(z, 33)
+    with pytest.raises(nv.Nvfp4Error):
+        nv.route(z, 0)
+    ids, w = nv.route(z[:0], 4)
+    assert ids.shape == (0, 4) and w.shape == (0, 4)
+
+
+def test_route_feeds_the_expert_ffn(nv):
+    """Routing and experts together: the ids and weights go into the expert FFN as
+    they are; a token with every expert masked gets a zero row."""
+    cfg = synth.TINY
+    x = dev_bf16(synth.activations(cfg))
+    w = [synth.expert_weights(cfg, e, device=DEV) for e in range(cfg.E)]
+    w1 = nv.quantize_experts(torch.stack([a for a, _ in w]))
+    w2 = nv.quantize_experts(torch.stack([b for _, b in w]))
+    z = _logits(cfg.T, cfg.E, 8)
+    z[5] = -INF
+    z[9, 1:] = -INF
+    ids, wt = _check(nv, z, cfg.topk)
+    a2 = dev_f32(cfg.a2_gs)
+    y = nv.moe_expert_ffn(x, ids, wt, *w1, *w2, a2, out_dtype=torch.float32)
+    want, ww = route_rows(host(z.double()), cfg.topk)
+    y2 = nv.moe_expert_ffn(x, torch.from_numpy(want).to(DEV), torch.from_numpy(ww.astype(np.float32)).to(DEV), *w1,
+                           *w2, a2, out_dtype=torch.float32)
+    assert (y[5] == 0).all() and (y[9] != 0).any()
+    # the weights differ by roundings only, and the FFN is linear in them
+    assert float((y - y2).norm() / y2.norm()) <= 64 * 2.0 ** -24
