@@ -288,6 +288,23 @@ int moe_expert_ffn_nvfp4(const nvfp4_moe_args *args, void *ws, size_t ws_bytes, 
 int moe_expert_ffn_nvfp4_noalloc(const nvfp4_moe_args *args, void *stream);
 
 /*
+ * moe_router_logits -- the router's gate projection, the product moe_route
+ * reads:  logits[t][e] = sum_k x[t][k] * w[e][k] (+ bias[e]).
+ *   x       bf16 [T][H], H % 32 == 0
+ *   w       [E][H], bf16 (w_dtype 0) or fp32 (1); 1 <= E <= 512
+ *   bias    nullable fp32 [E]
+ *   logits  fp32 [T][E]
+ *   Products are exact, also those of fp32 weights (whose 24 bits are used),
+ *   the accumulation is fp32 in a fixed order.  x, w and logits 16-byte
+ *   aligned; H at most 2^20, T at most 2^26 (else NVFP4_ERR_UNSUPPORTED).
+ *   Workspace: moe_router_logits_workspace_size bytes, 256-byte aligned (0:
+ *   none is needed and ws may be NULL).
+ */
+size_t moe_router_logits_workspace_size(int64_t T, int64_t H, int64_t E, int w_dtype);
+int moe_router_logits(const uint16_t *x, int64_t T, int64_t H, const void *w, int w_dtype, int64_t E,
+                      const float *bias, float *logits, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * moe_route -- the router's decision for T tokens: the k expert ids and
  * weights per token that moe_expert_ffn_nvfp4 takes (topk_ids, topk_w), from
  * the router's logits.

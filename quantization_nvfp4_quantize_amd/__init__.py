@@ -65,6 +65,8 @@ _SIG = {
     "mxfp4_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i64, ctypes.c_int, _vp, _vp]),
     "mxfp4_linear_workspace_size": (_sz, [_i64, _i64, _i64]),
     "mxfp4_linear": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _i64, ctypes.c_int, _vp, _vp, _sz, _vp]),
+    "moe_router_logits_workspace_size": (_sz, [_i64, _i64, _i64, ctypes.c_int]),
+    "moe_router_logits": (ctypes.c_int, [_vp, _i64, _i64, _vp, ctypes.c_int, _i64, _vp, _vp, _vp, _sz, _vp]),
     "moe_route": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _i64, ctypes.c_int,
                                  ctypes.c_int, ctypes.c_float, _vp, _vp, _vp, _vp]),
     "moe_expert_ffn_nvfp4_workspace_size": (_sz, [ctypes.POINTER(MoeArgs)]),
@@ -275,6 +277,35 @@ def _on(device, *tensors):
         if t is not None and t.device != device:
             raise ValueError(f"all tensors of a call must be on one device, got {device} and {t.device}")
     return torch.cuda.device(device) if torch.cuda.current_device() != device.index else contextlib.nullcontext()
+
+
+def router_logits(x, w, bias=None, out=None, ws=None):
+    """The router's gate projection: float32 logits [T][E] = x @ w^T (+ bias).
+    x bf16 [T][H] (H % 32 == 0); w [E][H] bf16 or float32 (all its bits are
+    used); bias float32 [E]."""
+    _require(x, torch.bfloat16, "x")
+    if w.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"w must be bfloat16 or float32, got {w.dtype}")
+    _require(w, w.dtype, "w")
+    _require(bias, torch.float32, "bias")
+    _require(out, torch.float32, "out")
+    if x.dim() != 2 or w.dim() != 2 or w.shape[1] != x.shape[1]:
+        raise ValueError(f"x must be [T][H] and w [E][H], got {tuple(x.shape)} and {tuple(w.shape)}")
+    (T, H), E, dev = x.shape, w.shape[0], x.device
+    if bias is not None and bias.shape != (E,):
+        raise ValueError(f"bias must be [{E}], got {tuple(bias.shape)}")
+    if out is None:
+        out = torch.empty((T, E), dtype=torch.float32, device=dev)
+    elif out.shape != (T, E):
+        raise ValueError(f"out must be [{T}][{E}], got {tuple(out.shape)}")
+    code = 0 if w.dtype == torch.bfloat16 else 1
+    with _on(dev, w, bias, out, ws):
+        if ws is None:
+            need = _lib.moe_router_logits_workspace_size(T, H, E, code)
+            ws = _workspace(need, dev) if need else None
+        _check(_lib.moe_router_logits(_p(x), T, H, _p(w), code, E, _p(bias), _p(out), _p(ws),
+                                      0 if ws is None else ws.numel(), _stream(dev)), "moe_router_logits")
+    return out
 
 
 _SCORING = {"softmax": 0, "sigmoid": 1}

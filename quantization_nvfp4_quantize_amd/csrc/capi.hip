@@ -268,6 +268,34 @@ int nvfp4_linear(const uint16_t* x, int64_t M, int64_t K, const float* x_gs_in, 
 }
 
 // ------------------------------------------------------------------ router
+size_t moe_router_logits_workspace_size(int64_t T, int64_t H, int64_t E, int w_dtype) {
+  if (T <= 0 || H <= 0 || E <= 0) return 0;
+  return nvfp4::router_logits_workspace_bytes(T, H, E, w_dtype == 0);
+}
+
+int moe_router_logits(const uint16_t* x, int64_t T, int64_t H, const void* w, int w_dtype, int64_t E,
+                      const float* bias, float* logits, void* ws, size_t ws_bytes, void* stream) {
+  g_last_error[0] = 0;
+  if (T < 0 || H < 1 || E < 1) return fail(NVFP4_ERR_INVALID_ARG, "moe_router_logits: need T >= 0, H >= 1, E >= 1");
+  if (w_dtype != 0 && w_dtype != 1)
+    return fail(NVFP4_ERR_INVALID_ARG, "moe_router_logits: w_dtype must be 0 (bf16) or 1 (fp32)");
+  if (H % 32 != 0 || E > 512 || H > ((int64_t)1 << 20) || T > ((int64_t)1 << 26))
+    return fail(NVFP4_ERR_UNSUPPORTED,
+                "moe_router_logits: need H %% 32 == 0, H <= 2^20, E <= 512 and T <= 2^26 (T=%lld H=%lld E=%lld)",
+                (long long)T, (long long)H, (long long)E);
+  if (T == 0) return NVFP4_OK;
+  if (!x || !w || !logits) return fail(NVFP4_ERR_INVALID_ARG, "moe_router_logits: null pointer");
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(logits, 16) || !aligned(bias, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "moe_router_logits: misaligned pointer (x, w and logits need 16 bytes)");
+  const size_t need = moe_router_logits_workspace_size(T, H, E, w_dtype);
+  if (need && (!ws || ws_bytes < need))
+    return fail(NVFP4_ERR_WORKSPACE, "moe_router_logits: workspace %zu < %zu bytes", ws_bytes, need);
+  if (need && !aligned(ws, 256)) return fail(NVFP4_ERR_INVALID_ARG, "moe_router_logits: ws must be 256-byte aligned");
+  return hip_status(nvfp4::launch_router_logits(x, T, (int)H, w, w_dtype == 0, (int)E, bias, logits, ws,
+                                                reinterpret_cast<hipStream_t>(stream)),
+                    "moe_router_logits");
+}
+
 int moe_route(const void* logits, int logits_dtype, int64_t T, int64_t E, int64_t k, int scoring, const float* bias,
               int64_t n_group, int64_t topk_group, int group_top, int renormalize, float scale,
               const int32_t* n_tokens, int32_t* ids, float* weights, void* stream) {

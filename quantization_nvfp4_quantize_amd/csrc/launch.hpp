@@ -140,6 +140,13 @@ hipError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, con
                             int n_group, int topk_group, int group_top, bool renormalize, float scale,
                             const int32_t* n_tokens, int32_t* ids, float* w, hipStream_t s);
 
+// ---- router_gemm.hip
+// logits [T][E] = x [T][H] (bf16) @ w [E][H]^T (bf16 or fp32) + bias (nullable
+// [E]); H % 32 == 0.  ws: router_logits_workspace_bytes, 256-byte aligned.
+size_t router_logits_workspace_bytes(int64_t T, int64_t H, int64_t E, bool w_bf16);
+hipError_t launch_router_logits(const uint16_t* x, int64_t T, int H, const void* w, bool w_bf16, int E,
+                                const float* bias, float* out, void* ws, hipStream_t s);
+
 // ---- mxfp4.hip (OCP MX v1.0 MXFP4: E8M0 scale per 32 elements, E2M1 elements)
 // n bf16 values (n % 32 == 0) -> q [n/2] (element 2i in the low nibble of
 // byte i), sc [n/32] E8M0 codes

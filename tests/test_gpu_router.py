@@ -237,3 +237,113 @@ def test_route_feeds_the_expert_ffn(nv):
     assert (y[5] == 0).all() and (y[9] != 0).any()
     # the weights differ by roundings only, and the FFN is linear in them
     assert float((y - y2).norm() / y2.norm()) <= 64 * 2.0 ** -24
+
+
+# ------------------------------------------------------------------ gate projection
+def _gate(T, H, E, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, H, generator=g).bfloat16()
+    w = (torch.randn(E, H, generator=g) * 0.02).to(dtype)
+    return x.to(DEV), w.to(DEV), (torch.randn(E, generator=g) * 0.1).to(DEV)
+
+
+def _gate_check(y, x, w, bias):
+    """Products are exact, so only the fp32 accumulation errs: at most H + 64
+    roundings of partial sums, none larger than the sum of the terms'
+    magnitudes; and over all elements like a walk of H / 8 + 20 steps (eight
+    or more products enter a sum at once, and the slices' sums are added),
+    each uniform within half a step of a partial sum (variance a third of its
+    square), allowed twice.  The terms are independent with mean zero, so a
+    partial sum of them has at most the mean square of the whole, which is the
+    sum of the terms' squares (the result itself may be smaller by cancellation
+    and says nothing about the sums on the way)."""
+    H = x.shape[1]
+    xd, wd = x.double(), w.double()
+    want, size = xd @ wd.t().contiguous(), xd.abs() @ wd.abs().t().contiguous()
+    square = xd.square() @ wd.square().t().contiguous()
+    if bias is not None:
+        want, size, square = want + bias.double(), size + bias.double().abs(), square + bias.double().square()
+    err = (y.double() - want).abs()
+    assert bool((err <= size * (H + 64) * 2.0 ** -24).all())
+    rel = float(err.norm() / square.sum().sqrt())
+    assert rel <= 2 * ((H / 8 + 20) / 3) ** 0.5 * 2.0 ** -24, rel
+
+
+GATE_SHAPES = [(1, 32, 1), (1, 7168, 256), (3, 64, 5), (16, 256, 8), (17, 96, 17), (33, 1280, 160), (100, 512, 511),
+               (129, 2048, 72), (130, 7168, 256), (300, 160, 512), (1000, 768, 40), (513, 1024, 128),
+               (2049, 480, 200), (4100, 256, 256)]
+
+
+@pytest.mark.parametrize("T,H,E", GATE_SHAPES)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_router_logits_shapes(nv, T, H, E, dtype):
+    x, w, b = _gate(T, H, E, dtype, T + H + E)
+    _gate_check(nv.router_logits(x, w), x, w, None)
+    out = torch.full((T, E), 9.0, device=DEV)
+    y = nv.router_logits(x, w, bias=b, out=out)
+    assert y is out
+    _gate_check(y, x, w, b)
+
+
+@pytest.mark.parametrize("T", [3, 700, 5000])
+def test_router_logits_uses_all_bits_of_a_32_bit_weight(nv, T):
+    """Differences of neighbouring weights: only the last bits are left, and
+    the answer is exact."""
+    H, E = 256, 40
+    w = torch.zeros(E, H, device=DEV)
+    g = torch.Generator().manual_seed(0)
+    v = (torch.rand(E, H // 2, generator=g) + 1.0).to(DEV)
+    nxt = torch.nextafter(v, torch.full_like(v, 2.0))
+    col = torch.arange(E, device=DEV)
+    w[col, 2 * col] = v[col, col]
+    w[col, 2 * col + 1] = nxt[col, col]
+    x = torch.zeros(T, H, device=DEV)
+    x[:, 0::2], x[:, 1::2] = -1.0, 1.0
+    y = nv.router_logits(x.bfloat16(), w)
+    assert torch.equal(y, (nxt - v)[col, col].expand(T, E))
+
+
+@pytest.mark.parametrize("T", [5, 600, 4500])
+def test_router_logits_rows_are_independent(nv, T):
+    """A token with NaN or infinite activations spoils its own row only."""
+    x, w, _ = _gate(T, 512, 96, torch.bfloat16, 3)
+    y0 = nv.router_logits(x, w)
+    x2 = x.clone()
+    x2[1], x2[T - 1, 7] = NAN, INF
+    y = nv.router_logits(x2, w)
+    keep = torch.ones(T, dtype=torch.bool, device=DEV)
+    keep[1] = keep[T - 1] = False
+    assert torch.equal(y[keep], y0[keep])
+    assert bool(torch.isnan(y[1]).all()) and not bool(torch.isfinite(y[T - 1]).any())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [7, 5000])
+def test_router_logits_graph_with_routing(nv, T, dtype):
+    """Projection and routing captured together, replayed on new inputs."""
+    x, w, b = _gate(T, 384, 64, dtype, 4)
+    nv.route(nv.router_logits(x, w, bias=b), 4)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = nv.router_logits(x, w, bias=b)
+        ids, wt = nv.route(y, 4)
+    for i in range(3):
+        x.copy_(_gate(T, 384, 64, dtype, 40 + i)[0])
+        g.replay()
+        y2 = nv.router_logits(x, w, bias=b)
+        i2, w2 = nv.route(y2, 4)
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(ids, i2) and torch.equal(wt, w2), i
+
+
+def test_router_logits_refuses_bad_tensors(nv):
+    x, w, b = _gate(4, 64, 8, torch.bfloat16, 1)
+    for args, kw in (((x, w[:, :32].contiguous()), {}), ((x, w.half()), {}), ((x.float(), w), {}),
+                     ((x, w), dict(bias=b[:7])), ((x, w), dict(out=torch.empty(4, 7, device=DEV))),
+                     ((x.t(), w), {}), ((x, w.cpu()), {}), ((x, w), dict(bias=b.double()))):
+        with pytest.raises(ValueError):
+            nv.router_logits(*args, **kw)
+    with pytest.raises(nv.Nvfp4Error):
+        nv.router_logits(x[:, :48].contiguous(), w[:, :48].contiguous())
+    assert nv.router_logits(x[:0], w).shape == (0, 8)

@@ -42,3 +42,33 @@ def test_route_binding_rejects_host_tensors(nv):
         nv.route(torch.zeros(4, 8), 2)
     with pytest.raises(ValueError, match="bfloat16 or float32"):
         nv.route(torch.zeros(4, 8, dtype=torch.float16), 2)
+
+
+def _logits(nv, x=FAKE, T=4, H=64, w=FAKE, w_dtype=0, E=8, bias=None, out=FAKE, ws=None, nws=0):
+    return nv._lib.moe_router_logits(x, T, H, w, w_dtype, E, bias, out, ws, nws, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), -1), (dict(H=0), -1), (dict(E=0), -1), (dict(w_dtype=2), -1), (dict(H=48), -2), (dict(E=513), -2),
+    (dict(H=(1 << 20) + 32), -2), (dict(T=(1 << 26) + 1), -2), (dict(x=None), -1), (dict(w=None), -1),
+    (dict(out=None), -1), (dict(x=ctypes.c_void_p(0x10008)), -1), (dict(w=ctypes.c_void_p(0x10004)), -1),
+    (dict(out=ctypes.c_void_p(0x10004)), -1), (dict(bias=ctypes.c_void_p(0x10001)), -1)])
+def test_router_logits_rejects(nv, kw, status):
+    assert _logits(nv, **kw) == status
+    assert b"moe_router_logits" in nv._lib.nvfp4_last_error()
+
+
+def test_router_logits_workspace_and_empty(nv):
+    assert _logits(nv, x=None, T=0, w=None, out=None) == 0
+    assert nv._lib.moe_router_logits_workspace_size(0, 64, 8, 0) == 0
+    for T, H, E, d in ((1, 64, 8, 0), (16384, 7168, 256, 0), (16384, 7168, 256, 1), (5000, 4096, 512, 1)):
+        need = nv._lib.moe_router_logits_workspace_size(T, H, E, d)
+        if need:
+            assert _logits(nv, T=T, H=H, E=E, w_dtype=d, ws=FAKE, nws=need - 1) == -3
+            assert b"workspace" in nv._lib.nvfp4_last_error()
+            assert _logits(nv, T=T, H=H, E=E, w_dtype=d, ws=ctypes.c_void_p(0x10010), nws=need) == -1
+
+
+def test_router_logits_binding_rejects_host_tensors(nv):
+    with pytest.raises(ValueError, match="GPU"):
+        nv.router_logits(torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(8, 64, dtype=torch.bfloat16))
