@@ -143,6 +143,33 @@ int nvfp4_linear(const uint16_t *x, int64_t M, int64_t K, const float *x_gs_in, 
                  float *x_gs_out, void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * nvfp4_lora_add -- the low-rank adapters of many requests, added to the output
+ * of a projection they share (nvfp4_linear, mxfp4_linear or any other):
+ *   out[t] = y[t] + scales[id] * b[id] (a[id] x[t]),  id = ids[t]
+ * for tokens with 0 <= id < L, and out[t] = y[t] for the others (a request
+ * without an adapter, the rows behind a padded batch).
+ *   y       [T][N], bf16 (dtype 0) or fp32 (1): the projection's output
+ *   x       bf16 [T][K]: the projection's input
+ *   a       bf16 [L][r][K];  b bf16 [L][N][r].  Adapters of a smaller rank
+ *           are padded with zeros.
+ *   ids     int32 [T], scales nullable fp32 [L] (1 without)
+ *   out     [T][N], the type of y; y itself (in place) or a buffer that does
+ *           not overlap it.  In place, rows without an adapter are not touched.
+ *   Products are exact and accumulated in fp32; a[id] x[t] goes into the
+ *   second product with 16 bits (bf16 output) or 24 (fp32); one rounding of
+ *   the sum to the output's type.  A token's result does not depend on the
+ *   other tokens of the call beyond the fp32 summation order of a[id] x[t].
+ *   T >= 0; K % 32 == 0, N % 8 == 0, r % 8 == 0, r <= 128, L <= 512 and T, K,
+ *   N <= 2^20 (else NVFP4_ERR_UNSUPPORTED).  y, x, a, b, out
+ *   16-byte aligned.  Workspace: nvfp4_lora_add_workspace_size bytes, 256-byte
+ *   aligned; calls that may overlap in time need one each.
+ */
+size_t nvfp4_lora_add_workspace_size(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L);
+int nvfp4_lora_add(const void *y, int dtype, int64_t T, int64_t N, const uint16_t *x, int64_t K, const uint16_t *a,
+                   const uint16_t *b, int64_t r, int64_t L, const int32_t *ids, const float *scales, void *out,
+                   void *ws, size_t ws_bytes, void *stream);
+
+/*
  * nvfp4_pair_scales -- a weight block-scale matrix sf [R][C] (C = K/16 bytes
  * per row) rewritten once, at weight preparation, in the row-paired layout
  * the 32-row MoE tiles read (nvfp4_moe_args.w1_sf_paired, w2_sf_paired):
@@ -296,7 +323,7 @@ int moe_expert_ffn_nvfp4_noalloc(const nvfp4_moe_args *args, void *stream);
  *   logits  fp32 [T][E]
  *   Products are exact, also those of fp32 weights (whose 24 bits are used),
  *   the accumulation is fp32 in a fixed order.  x, w and logits 16-byte
- *   aligned; H at most 2^20, T at most 2^26 (else NVFP4_ERR_UNSUPPORTED).
+ *   aligned; H and T at most 2^20 (else NVFP4_ERR_UNSUPPORTED).
  *   Workspace: moe_router_logits_workspace_size bytes, 256-byte aligned (0:
  *   none is needed and ws may be NULL).
  */
@@ -330,8 +357,8 @@ int moe_router_logits(const uint16_t *x, int64_t T, int64_t H, const void *w, in
  *           routed; the rows behind them get id -1 and weight 0 (a padded
  *           batch, also in a captured graph)
  * Requirements: T >= 0, 1 <= E <= 512, 1 <= k <= 32 (else
- * NVFP4_ERR_UNSUPPORTED above those), n_group divides E and is at most 64,
- * 1 <= topk_group <= n_group, k <= topk_group * (E / n_group), T * k <= 2^30;
+ * NVFP4_ERR_UNSUPPORTED), n_group divides E and is at most 64,
+ * 1 <= topk_group <= n_group, k <= topk_group * (E / n_group), T <= 2^24;
  * logits aligned to 16 bytes.  No workspace; ids and weights must not overlap
  * the logits.
  */

@@ -65,6 +65,9 @@ _SIG = {
     "mxfp4_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i64, ctypes.c_int, _vp, _vp]),
     "mxfp4_linear_workspace_size": (_sz, [_i64, _i64, _i64]),
     "mxfp4_linear": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _i64, ctypes.c_int, _vp, _vp, _sz, _vp]),
+    "nvfp4_lora_add_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "nvfp4_lora_add": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp,
+                                      _vp, _sz, _vp]),
     "moe_router_logits_workspace_size": (_sz, [_i64, _i64, _i64, ctypes.c_int]),
     "moe_router_logits": (ctypes.c_int, [_vp, _i64, _i64, _vp, ctypes.c_int, _i64, _vp, _vp, _vp, _sz, _vp]),
     "moe_route": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _i64, ctypes.c_int,
@@ -122,6 +125,15 @@ def _workspace(nbytes, device):
     the graph lives.  (The allocator caches freed blocks, so a call of the
     same size costs no device allocation.)"""
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+
+
+def _on(device, *tensors):
+    """The device to launch on (a context manager): that of the call's tensors,
+    all of which must be there."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors of a call must be on one device, got {device} and {t.device}")
+    return torch.cuda.device(device) if torch.cuda.current_device() != device.index else contextlib.nullcontext()
 
 
 # ------------------------------------------------------------------ API
@@ -218,6 +230,45 @@ def linear_workspace(M, K, N, device):
                        device=device)
 
 
+def lora_add(y, x, a, b, ids, scales=None, out=None, ws=None):
+    """The low-rank adapters of many requests, added to the output y of a
+    projection they share (linear, mx_linear or another):
+    out[t] = y[t] + scales[id] * b[id] @ (a[id] @ x[t]) with id = ids[t], and
+    out[t] = y[t] for tokens whose id is outside [0, L).
+
+    y [T][N] bf16 or float32; x bf16 [T][K]: the projection's input; a bf16
+    [L][r][K], b bf16 [L][N][r] (smaller ranks padded with zeros); ids int32
+    [T]; scales float32 [L].  out: a new tensor by default; pass y to work in
+    place.  ws: a workspace of lora_add_workspace, not shared by calls that may
+    run at the same time."""
+    if y.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"y must be bfloat16 or float32, got {y.dtype}")
+    for t, d, n in ((y, y.dtype, "y"), (x, torch.bfloat16, "x"), (a, torch.bfloat16, "a"), (b, torch.bfloat16, "b"),
+                    (ids, torch.int32, "ids"), (scales, torch.float32, "scales"), (out, y.dtype, "out")):
+        _require(t, d, n)
+    if y.dim() != 2 or x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("y and x must be matrices, a [L][r][K] and b [L][N][r]")
+    (T, N), K, (L, r, _), dev = y.shape, x.shape[1], a.shape, y.device
+    for t, shape, n in ((x, (T, K), "x"), (a, (L, r, K), "a"), (b, (L, N, r), "b"), (ids, (T,), "ids"),
+                        (scales, (L,), "scales"), (out, (T, N), "out")):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{n} must be {list(shape)}, got {list(t.shape)}")
+    if out is None:
+        out = torch.empty_like(y)
+    with _on(dev, x, a, b, ids, scales, out, ws):
+        if ws is None:
+            ws = _workspace(_lib.nvfp4_lora_add_workspace_size(T, N, K, r, L), dev)
+        _check(_lib.nvfp4_lora_add(_p(y), 0 if y.dtype == torch.bfloat16 else 1, T, N, _p(x), K, _p(a), _p(b), r, L,
+                                   _p(ids), _p(scales), _p(out), _p(ws), ws.numel(), _stream(dev)), "nvfp4_lora_add")
+    return out
+
+
+def lora_add_workspace(T, N, K, r, L, device):
+    """A dedicated workspace for nvfp4_lora_add (e.g. for graph capture)."""
+    return torch.empty(max(int(_lib.nvfp4_lora_add_workspace_size(T, N, K, r, L)), 256), dtype=torch.uint8,
+                       device=device)
+
+
 # ------------------------------------------------------------------ MXFP4
 # The separately labelled OCP MX v1.0 format (E8M0 scale per 32 elements) on
 # the scaled FP4 MFMA; not the NVFP4 of the functions above.
@@ -270,15 +321,6 @@ def mx_linear_workspace(M, K, N, device):
 
 
 # ------------------------------------------------------------------ router
-def _on(device, *tensors):
-    """The device to launch on (a context manager): that of the call's tensors,
-    all of which must be there."""
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors of a call must be on one device, got {device} and {t.device}")
-    return torch.cuda.device(device) if torch.cuda.current_device() != device.index else contextlib.nullcontext()
-
-
 def router_logits(x, w, bias=None, out=None, ws=None):
     """The router's gate projection: float32 logits [T][E] = x @ w^T (+ bias).
     x bf16 [T][H] (H % 32 == 0); w [E][H] bf16 or float32 (all its bits are

@@ -279,9 +279,9 @@ int moe_router_logits(const uint16_t* x, int64_t T, int64_t H, const void* w, in
   if (T < 0 || H < 1 || E < 1) return fail(NVFP4_ERR_INVALID_ARG, "moe_router_logits: need T >= 0, H >= 1, E >= 1");
   if (w_dtype != 0 && w_dtype != 1)
     return fail(NVFP4_ERR_INVALID_ARG, "moe_router_logits: w_dtype must be 0 (bf16) or 1 (fp32)");
-  if (H % 32 != 0 || E > 512 || H > ((int64_t)1 << 20) || T > ((int64_t)1 << 26))
+  if (H % 32 != 0 || E > 512 || H > ((int64_t)1 << 20) || T > ((int64_t)1 << 20))
     return fail(NVFP4_ERR_UNSUPPORTED,
-                "moe_router_logits: need H %% 32 == 0, H <= 2^20, E <= 512 and T <= 2^26 (T=%lld H=%lld E=%lld)",
+                "moe_router_logits: need H %% 32 == 0, H <= 2^20, E <= 512 and T <= 2^20 (T=%lld H=%lld E=%lld)",
                 (long long)T, (long long)H, (long long)E);
   if (T == 0) return NVFP4_OK;
   if (!x || !w || !logits) return fail(NVFP4_ERR_INVALID_ARG, "moe_router_logits: null pointer");
@@ -316,7 +316,7 @@ int moe_route(const void* logits, int logits_dtype, int64_t T, int64_t E, int64_
   if (k > topk_group * (E / n_group))
     return fail(NVFP4_ERR_INVALID_ARG, "moe_route: k %lld exceeds the %lld experts of topk_group groups", (long long)k,
                 (long long)(topk_group * (E / n_group)));
-  if (T > ((int64_t)1 << 30) / k) return fail(NVFP4_ERR_UNSUPPORTED, "moe_route: too many (token, expert) pairs");
+  if (T > ((int64_t)1 << 24)) return fail(NVFP4_ERR_UNSUPPORTED, "moe_route: need T <= 2^24");
   if (T == 0) return NVFP4_OK;
   if (!logits || !ids || !weights) return fail(NVFP4_ERR_INVALID_ARG, "moe_route: null pointer");
   if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(n_tokens, 4) || !aligned(ids, 4) || !aligned(weights, 4))
@@ -325,6 +325,52 @@ int moe_route(const void* logits, int logits_dtype, int64_t T, int64_t E, int64_
                                             (int)n_group, (int)topk_group, group_top, renormalize == 1, scale,
                                             n_tokens, ids, weights, reinterpret_cast<hipStream_t>(stream)),
                     "moe_route");
+}
+
+// ------------------------------------------------------------------ adapters
+namespace {
+bool lora_sizes_ok(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
+  return T >= 0 && N >= 1 && K >= 1 && r >= 1 && L >= 1;
+}
+bool lora_supported(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
+  return K % 32 == 0 && N % 8 == 0 && r % 8 == 0 && r <= 128 && L <= 512 && T <= ((int64_t)1 << 20) &&
+         K <= ((int64_t)1 << 20) && N <= ((int64_t)1 << 20);
+}
+}  // namespace
+
+size_t nvfp4_lora_add_workspace_size(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
+  if (!lora_sizes_ok(T, N, K, r, L) || !lora_supported(T, N, K, r, L) || T == 0) return 0;
+  return nvfp4::lora_workspace_bytes(T, (int)r, (int)L);
+}
+
+int nvfp4_lora_add(const void* y, int dtype, int64_t T, int64_t N, const uint16_t* x, int64_t K, const uint16_t* a,
+                   const uint16_t* b, int64_t r, int64_t L, const int32_t* ids, const float* scales, void* out,
+                   void* ws, size_t ws_bytes, void* stream) {
+  g_last_error[0] = 0;
+  if (!lora_sizes_ok(T, N, K, r, L))
+    return fail(NVFP4_ERR_INVALID_ARG, "nvfp4_lora_add: need T >= 0 and N, K, r, L >= 1");
+  if (dtype != 0 && dtype != 1) return fail(NVFP4_ERR_INVALID_ARG, "nvfp4_lora_add: dtype must be 0 (bf16) or 1 (fp32)");
+  if (!lora_supported(T, N, K, r, L))
+    return fail(NVFP4_ERR_UNSUPPORTED,
+                "nvfp4_lora_add: need K %% 32 == 0, N %% 8 == 0, r %% 8 == 0, r <= 128, L <= 512 and T, K, N "
+                "<= 2^20 (T=%lld N=%lld K=%lld r=%lld L=%lld)",
+                (long long)T, (long long)N, (long long)K, (long long)r, (long long)L);
+  if (T == 0) return NVFP4_OK;
+  if (!y || !x || !a || !b || !ids || !out) return fail(NVFP4_ERR_INVALID_ARG, "nvfp4_lora_add: null pointer");
+  if (!aligned(y, 16) || !aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16) ||
+      !aligned(ids, 4) || !aligned(scales, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "nvfp4_lora_add: misaligned pointer (y, x, a, b and out need 16 bytes)");
+  const size_t bytes = (size_t)T * (size_t)N * (dtype == 0 ? 2 : 4);
+  if (out != y && static_cast<const char*>(y) < static_cast<char*>(out) + bytes &&
+      static_cast<char*>(out) < static_cast<const char*>(y) + bytes)
+    return fail(NVFP4_ERR_INVALID_ARG, "nvfp4_lora_add: y and out overlap (give the same pointer to work in place)");
+  const size_t need = nvfp4::lora_workspace_bytes(T, (int)r, (int)L);
+  if (!ws || ws_bytes < need)
+    return fail(NVFP4_ERR_WORKSPACE, "nvfp4_lora_add: workspace %zu < %zu bytes", ws_bytes, need);
+  if (!aligned(ws, 256)) return fail(NVFP4_ERR_INVALID_ARG, "nvfp4_lora_add: ws must be 256-byte aligned");
+  return hip_status(nvfp4::launch_lora_add(y, dtype == 0, T, N, x, (int)K, a, b, (int)r, (int)L, ids, scales, out, ws,
+                                           reinterpret_cast<hipStream_t>(stream)),
+                    "nvfp4_lora_add");
 }
 
 // ------------------------------------------------------------------ MXFP4
