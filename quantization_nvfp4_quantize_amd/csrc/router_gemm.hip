@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "gemm_common.hpp"
 #include "launch.hpp"
@@ -64,15 +65,15 @@ __device__ __forceinline__ Split3 split3(const float4& a, const float4& b) {
   return s;
 }
 
-// ---- one to four tokens: a workgroup per expert, every thread a few 16-byte
+// ---- up to eight tokens: a workgroup per expert, every thread a few 16-byte
 // chunks of the row, all of them requested at once: one launch that lasts one
 // trip to memory.  fp32 fused multiply-adds keep the products exact.
 constexpr int kDotThreads = 256;
-constexpr int kDotTokens = 4;
+constexpr int kDotTokens = 8;
 
 template <bool F32W, int NT>
 __global__ __launch_bounds__(kDotThreads) void gate_dot_kernel(GateParams p) {
-  constexpr int kUnroll = 4;
+  constexpr int kUnroll = NT <= 4 ? 4 : 2;
   __shared__ float part[kDotThreads / 64][NT];
   const int e = blockIdx.x, tid = threadIdx.x, chunks = p.H / 8;
   float acc[NT];
@@ -157,7 +158,7 @@ __global__ __launch_bounds__(64 * kSliceWaves) void gate_slice_kernel(GateParams
   const uint16_t* xr = p.x + min(t0 + r, p.T - 1) * p.H + 8 * g;
   const int64_t wo = (int64_t)min(e0 + r, p.E - 1) * p.H + 8 * g;
   const int nk = p.H / 16, share = p.slices * kSliceWaves, mine = slice * kSliceWaves + wave;
-  const int k0 = (int)((int64_t)nk * mine / share), k1 = (int)((int64_t)nk * (mine + 1) / share);
+  const int k0 = (int)((uint32_t)(nk * mine) / (uint32_t)share), k1 = (int)((uint32_t)(nk * (mine + 1)) / (uint32_t)share);
   f32x16 acc = {};
   for (int k = k0; k < k1; k += kSteps) {
     uint4 a[kSteps];
@@ -204,17 +205,25 @@ __global__ __launch_bounds__(64 * kSliceWaves) void gate_slice_kernel(GateParams
   }
 }
 
-// ---- many tokens: 128 tokens x 128 experts per workgroup, 64 x 64 per wave
-// (2 x 2 MFMA tiles of 32 x 32), K in steps of 64 through four LDS stages
-// filled by direct loads three steps ahead.  Chunk c (16 bytes) of a row lies
-// at c ^ swz_key(row).  With too few tiles for the chip, K is sliced as well;
-// an fp32 weight comes as three bf16 planes (gate_planes_kernel), each a
-// partial sum of its own.
+// ---- many tokens: 128 tokens x 128 experts per workgroup, K in steps of 64
+// through four LDS stages filled by direct loads.  Of the eight waves four
+// take the first half of every step and four the second, 64 x 64 outputs each
+// (2 x 2 MFMA tiles), and the halves are added at the end; the fragments of
+// the next step are read before this step's MFMAs.  Chunk c (16 bytes) of a row
+// lies at c ^ swz_key(row).  The experts are the MFMA's rows, so that a lane
+// ends with four experts of one token in a register quad, which is one store.
+// The direct loads alone (32 KiB a step and CU) take 50 of the 63 us of T16384
+// H7168 E256, 40 when all of them hit the L2.  64 x 128 outputs per wave over
+// quarters of a step, a quarter less LDS traffic, gain 1 % there and lose 10 %
+// below 4096 tokens.  The time outside the loop counts as well: an epilogue that
+// sent all sums through LDS and stored single floats took 16000 cycles.
+// With too few tiles for the chip, K is sliced as well; an fp32 weight comes as
+// three bf16 planes (gate_planes_kernel), each a partial sum of its own.
 constexpr int kTileRows = 128;
 constexpr int kTileStages = 4;
 constexpr int kTileOperand = kTileRows * 8;  // 16-byte chunks of one operand's stage
 
-__global__ __launch_bounds__(256) void gate_tile_kernel(GateParams p) {
+__global__ __launch_bounds__(512) void gate_tile_kernel(GateParams p) {
   __shared__ uint4 lds[kTileStages * 2 * kTileOperand];
   const int etiles = (p.E + kTileRows - 1) / kTileRows;
   const int ttiles = (int)((p.T + kTileRows - 1) / kTileRows);
@@ -226,72 +235,117 @@ __global__ __launch_bounds__(256) void gate_tile_kernel(GateParams p) {
   const int64_t t0 = (int64_t)(tile / etiles) * kTileRows;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int steps = p.H / 64;
-  const int s0 = (int)((int64_t)steps * slice / p.slices), s1 = (int)((int64_t)steps * (slice + 1) / p.slices);
+  const int s0 = (int)((uint32_t)(steps * slice) / (uint32_t)p.slices);
+  const int s1 = (int)((uint32_t)(steps * (slice + 1)) / (uint32_t)p.slices);
   const uint32_t row_bytes = 2u * (uint32_t)p.H;
   const uint8_t* xb = reinterpret_cast<const uint8_t*>(p.x) + t0 * row_bytes;
   const uint8_t* wb = static_cast<const uint8_t*>(p.w) + ((int64_t)plane * p.E + e0) * row_bytes;
   const int trows = (int)min((int64_t)kTileRows, p.T - t0), erows = min(kTileRows, p.E - e0);
-  // load u of a wave: rows 32 wave + 8 u .. + 7 of each operand, 128 bytes each
-  uint32_t xo[4], wo[4];
+  // load u of a wave: rows 16 wave + 8 u .. + 7 of each operand, 128 bytes each
+  uint32_t xo[2], wo[2];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int row = 32 * wave + 8 * u + (lane >> 3);
+  for (int u = 0; u < 2; ++u) {
+    const int row = 16 * wave + 8 * u + (lane >> 3);
     const uint32_t chunk = 16u * (uint32_t)((lane & 7) ^ swz_key(row));
     xo[u] = (uint32_t)min(row, trows - 1) * row_bytes + chunk;  // rows past the end repeat the last one
     wo[u] = (uint32_t)min(row, erows - 1) * row_bytes + chunk;
   }
   auto load = [&](int step, int stage) {
-    uint4* dst = lds + stage * 2 * kTileOperand + 32 * 8 * wave;
+    uint4* dst = lds + stage * 2 * kTileOperand + 16 * 8 * wave;
     const size_t at = (size_t)step * 128;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 2; ++u) {
       dma16s(reinterpret_cast<f16x8*>(dst + 64 * u), xb + at, xo[u]);
       dma16s(reinterpret_cast<f16x8*>(dst + kTileOperand + 64 * u), wb + at, wo[u]);
     }
   };
-  const int wm = wave >> 1, wn = wave & 1, r = lane & 31, g = lane >> 5;
-  const uint4 *fa[2], *fb[2];
-  int ka[2], kb[2];
+  // rows 32 i + r of either operand, chunks 4 half + 2 q + g; the key of a row
+  // depends on r and on the parity of i, and chunk c ^ 2 lies at address ^ 2
+  const int half = wave >> 2, wm = (wave >> 1) & 1, wn = wave & 1, r = lane & 31, g = lane >> 5;
+  const int c0 = (4 * half + g) ^ swz_key(r), c1 = (4 * half + g) ^ swz_key(32 + r);
+  const uint4* const fx = lds + 8 * (64 * wm + r);
+  const uint4* const fw = lds + kTileOperand + 8 * (64 * wn + r);
+  struct Frags {
+    uint4 x[2][2], w[2][2];  // [q][i]
+  };
+  auto read = [&](int stage, Frags& f) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int ra = 64 * wm + 32 * i + r, rb = 64 * wn + 32 * i + r;
-    fa[i] = lds + 8 * ra;
-    fb[i] = lds + kTileOperand + 8 * rb;
-    ka[i] = swz_key(ra);
-    kb[i] = swz_key(rb);
-  }
-  f32x16 acc[2][2] = {};
-#pragma unroll
-  for (int i = 0; i < kTileStages - 1; ++i) load(min(s0 + i, s1 - 1), i);
-  for (int s = s0; s < s1; ++s) {
-    const int stage = (s - s0) & (kTileStages - 1);
-    // 8 loads a step: two later steps may still be on their way
-    wait_vmcnt<16>();
-    lds_barrier();  // stage s has landed for every wave, and stage s - 1 has been read by every wave
-    load(min(s + kTileStages - 1, s1 - 1), (stage + kTileStages - 1) & (kTileStages - 1));
-    const int so = stage * 2 * kTileOperand;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint4 a[2], b[2];
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        a[i] = fa[i][so + ((2 * q + g) ^ ka[i])];
-        b[i] = fb[i][so + ((2 * q + g) ^ kb[i])];
+        const int at = stage * 2 * kTileOperand + 256 * i + ((i ? c1 : c0) ^ (2 * q));
+        f.x[q][i] = fx[at];
+        f.w[q][i] = fw[at];
       }
+  };
+  f32x16 acc[2][2] = {};  // [token tile][expert tile]
+  // One step: its fragments are in cur.  The barrier publishes the stage of
+  // the next step and ends every wave's reads of this one's, which the load of
+  // step s + 4 then fills; 4 loads a step, so with at most 8 on their way all
+  // but those of steps s + 2 and s + 3 have landed.
+  auto body = [&](int s, const Frags& cur, Frags& nxt) {
+    const int stage = (s - s0) & (kTileStages - 1);
+    wait_vmcnt<8>();
+    lds_barrier();
+    SCHED_FENCE();
+    read((stage + 1) & (kTileStages - 1), nxt);
+    load(min(s + kTileStages, s1 - 1), stage);
+    SCHED_FENCE();
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mfma32(a[i], b[j], acc[i][j]);
-    }
+        for (int j = 0; j < 2; ++j) acc[i][j] = mfma32(cur.w[q][j], cur.x[q][i], acc[i][j]);
+    SCHED_FENCE();
+  };
+#pragma unroll
+  for (int i = 0; i < kTileStages; ++i) load(min(s0 + i, s1 - 1), i);
+  Frags even, odd;
+  wait_vmcnt<12>();
+  lds_barrier();
+  read(0, even);
+  for (int s = s0;;) {
+    body(s, even, odd);
+    if (++s == s1) break;
+    body(s, odd, even);
+    if (++s == s1) break;
   }
-  wait_vmcnt<0>();  // nothing may still be on its way into LDS when the workgroup ends
+  wait_vmcnt<0>();  // the last loads go into stages that nobody reads any more
+  // Each half hands one token tile's sums to the other and keeps the other
+  // tile (first half: token tile 0): 8 KiB of LDS per wave, quad by quad
+  f32x4* const sum = reinterpret_cast<f32x4*>(lds);
+  auto quad = [](const f32x16& v, int i) { return f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]}; };
+  __syncthreads();
+  f32x16 keep[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int j = 0; j < 2; ++j) {
+    keep[j] = half ? acc[1][j] : acc[0][j];
+    const f32x16 give = half ? acc[0][j] : acc[1][j];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int v = 0; v < 4; ++v) sum[512 * wave + 64 * (4 * j + v) + lane] = quad(give, v);
+  }
+  __syncthreads();
+  const int64_t t = t0 + 64 * wm + 32 * half + r;
+  float* const out = p.out + ((int64_t)part * p.T + t) * p.E;
+  const bool vec = p.E % 4 == 0, biased = p.parts == 1 && p.bias;
 #pragma unroll
-      for (int v = 0; v < 16; ++v)
-        store_logit(p, part, t0 + 64 * wm + 32 * i + acc_row(v, lane), e0 + 64 * wn + 32 * j + r, acc[i][j][v]);
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const f32x4 o = sum[512 * (wave ^ 4) + 64 * (4 * j + v) + lane];
+      f32x4 y = quad(keep[j], v);
+      y = half ? o + y : y + o;  // the first half of K first
+      const int e = e0 + 64 * wn + 32 * j + 8 * v + 4 * g;
+      if (t >= p.T || e >= p.E) continue;
+      if (vec) {
+        if (biased) y += f32x4{p.bias[e], p.bias[e + 1], p.bias[e + 2], p.bias[e + 3]};
+        *reinterpret_cast<f32x4*>(out + e) = y;
+      } else {
+        for (int u = 0; u < 4; ++u)
+          if (e + u < p.E) out[e + u] = biased ? y[u] + p.bias[e + u] : y[u];
+      }
+    }
 }
 
 // fp32 weights -> three bf16 planes [3][n] that add up to them, the smallest first.
@@ -321,22 +375,27 @@ __global__ __launch_bounds__(256) void gate_sum_kernel(const float* __restrict__
       v.w += w.w;
     }
     if (bias) {
-      v.x += bias[i % E];
-      v.y += bias[(i + 1) % E];
-      v.z += bias[(i + 2) % E];
-      v.w += bias[(i + 3) % E];
+      const uint32_t e = (uint32_t)i % (uint32_t)E;  // at most 2^29 logits
+      float* y = &v.x;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) y[u] += bias[e + u < (uint32_t)E ? e + u : (e + u) % (uint32_t)E];
     }
     *reinterpret_cast<float4*>(out + i) = v;
   } else {
     for (int64_t j = i; j < min(i + 4, n); ++j) {
       float v = 0.0f;
       for (int q = 0; q < parts; ++q) v += part[q * n + j];
-      out[j] = bias ? v + bias[j % E] : v;
+      out[j] = bias ? v + bias[(uint32_t)j % (uint32_t)E] : v;
     }
   }
 }
 
-// Which kernel takes a call, and its workspace.
+// Which kernel takes a call, and its workspace.  Measured (us, bf16 H7168
+// E256 unless said otherwise): dot against slices at 8 tokens 6.0 / 8.0, at 12
+// 9.4 / 8.2; slices against tiles at 256 tokens 12.8 / 14.2, at 512 20.7 / 14.9;
+// fp32 weights, whose tiles cost three times as much, by the work of the
+// slices: H7168 E256 at 256 tokens 17.2 / 23.7, at 512 28.3 / 24.7; H4096 E72 at
+// 1024 tokens 13.2 / 18.8; H2048 E64 at 2048 tokens 12.1 / 17.4.
 struct GatePlan {
   enum Kind { kDot, kSlice, kTile } kind;
   int slices, parts;
@@ -348,16 +407,25 @@ GatePlan gate_plan(int64_t T, int64_t H, int64_t E, bool w_bf16) {
   if (T <= kDotTokens) return g;
   const int64_t big = (T + kTileRows - 1) / kTileRows * ((E + kTileRows - 1) / kTileRows);
   const int64_t small = (T + kSliceTile - 1) / kSliceTile * ((E + kSliceTile - 1) / kSliceTile);
-  if (T <= 512 || H % 64 != 0) {
+  if (H % 64 != 0 || (w_bf16 ? T <= 256 : small * H <= 1 << 19)) {
     g.kind = GatePlan::kSlice;
-    // about a workgroup per CU, a multiple of the 8 XCDs, four K steps of 16 or more per wave
+    // about a workgroup per CU and four K steps of 16 or more per wave;
+    // multiples of the 8 XCDs, or with a short K a power of two
     const int64_t want = std::min<int64_t>((256 + small - 1) / small, H / 16 / (4 * kSliceWaves));
-    g.slices = want >= 8 ? (int)std::min<int64_t>(want / 8 * 8, 32) : small < 256 ? (int)std::max<int64_t>(want, 1) : 1;
+    if (want >= 8)
+      g.slices = (int)std::min<int64_t>(want / 8 * 8, 32);
+    else if (small <= 256)
+      g.slices = H >= 4096 ? 8 : want >= 4 ? 4 : want >= 2 ? 2 : 1;
     g.parts = g.slices;
   } else {
     g.kind = GatePlan::kTile;
     const int planes = w_bf16 ? 1 : 3;
-    const int64_t want = std::min<int64_t>(256 / (big * planes), H / 64 / 4);
+    // as many slices as fill the chip, unless the partial sums cost more than
+    // the shorter loops save: a step takes 0.45 us, a partial logit 8 bytes
+    // written and read at 5 TB/s, so that steps / n * 0.45 us + n * T E * 1.6 ps
+    // is least at n^2 = 4400 H / (T E)
+    const int64_t want = std::min<int64_t>({256 / (big * planes), H / 64 / 4,
+                                            (int64_t)std::sqrt(4400.0 * H / ((double)T * E * planes))});
     g.slices = (int)std::max<int64_t>(want, 1);
     g.parts = g.slices * planes;
   }
@@ -378,12 +446,13 @@ hipError_t launch_router_logits(const uint16_t* x, int64_t T, int H, const void*
   const GatePlan g = gate_plan(T, H, E, w_bf16);
   GateParams p{x, w, bias, g.parts > 1 ? static_cast<float*>(ws) : out, T, H, E, g.parts, g.slices};
   if (g.kind == GatePlan::kDot) {
-    const int nt = T == 1 ? 1 : T == 2 ? 2 : 4;
-    auto go = [&](auto kernel) { kernel<<<E, kDotThreads, 0, s>>>(p); };
+        auto go = [&](auto one, auto two, auto four, auto eight) {
+      (T == 1 ? one : T == 2 ? two : T <= 4 ? four : eight)<<<E, kDotThreads, 0, s>>>(p);
+    };
     if (w_bf16)
-      nt == 1 ? go(gate_dot_kernel<false, 1>) : nt == 2 ? go(gate_dot_kernel<false, 2>) : go(gate_dot_kernel<false, 4>);
+      go(gate_dot_kernel<false, 1>, gate_dot_kernel<false, 2>, gate_dot_kernel<false, 4>, gate_dot_kernel<false, 8>);
     else
-      nt == 1 ? go(gate_dot_kernel<true, 1>) : nt == 2 ? go(gate_dot_kernel<true, 2>) : go(gate_dot_kernel<true, 4>);
+      go(gate_dot_kernel<true, 1>, gate_dot_kernel<true, 2>, gate_dot_kernel<true, 4>, gate_dot_kernel<true, 8>);
     return hipGetLastError();
   }
   if (g.kind == GatePlan::kSlice) {
@@ -398,7 +467,7 @@ hipError_t launch_router_logits(const uint16_t* x, int64_t T, int H, const void*
       p.w = planes;
     }
     const int64_t items = (T + kTileRows - 1) / kTileRows * ((E + kTileRows - 1) / kTileRows) * g.parts;
-    gate_tile_kernel<<<(unsigned)((items + 7) / 8 * 8), 256, 0, s>>>(p);
+    gate_tile_kernel<<<(unsigned)((items + 7) / 8 * 8), 512, 0, s>>>(p);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || g.parts == 1) return e;
