@@ -340,7 +340,7 @@ bool lora_supported(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
 
 size_t nvfp4_lora_add_workspace_size(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
   if (!lora_sizes_ok(T, N, K, r, L) || !lora_supported(T, N, K, r, L) || T == 0) return 0;
-  return nvfp4::lora_workspace_bytes(T, (int)r, (int)L);
+  return nvfp4::lora_workspace_bytes(T, (int)K, (int)r, (int)L);
 }
 
 int nvfp4_lora_add(const void* y, int dtype, int64_t T, int64_t N, const uint16_t* x, int64_t K, const uint16_t* a,
@@ -364,7 +364,7 @@ int nvfp4_lora_add(const void* y, int dtype, int64_t T, int64_t N, const uint16_
   if (out != y && static_cast<const char*>(y) < static_cast<char*>(out) + bytes &&
       static_cast<char*>(out) < static_cast<const char*>(y) + bytes)
     return fail(NVFP4_ERR_INVALID_ARG, "nvfp4_lora_add: y and out overlap (give the same pointer to work in place)");
-  const size_t need = nvfp4::lora_workspace_bytes(T, (int)r, (int)L);
+  const size_t need = nvfp4::lora_workspace_bytes(T, (int)K, (int)r, (int)L);
   if (!ws || ws_bytes < need)
     return fail(NVFP4_ERR_WORKSPACE, "nvfp4_lora_add: workspace %zu < %zu bytes", ws_bytes, need);
   if (!aligned(ws, 256)) return fail(NVFP4_ERR_INVALID_ARG, "nvfp4_lora_add: ws must be 256-byte aligned");

@@ -151,7 +151,7 @@ hipError_t launch_router_logits(const uint16_t* x, int64_t T, int H, const void*
 // out [T][N] = y + scales[id] * (x @ a[id]^T) @ b[id]^T for tokens with 0 <=
 // id < L, y for the others; K % 32 == 0, N % 8 == 0, r % 8 == 0, r <= 128,
 // L <= 512.  ws: lora_workspace_bytes, 256-byte aligned.
-size_t lora_workspace_bytes(int64_t T, int r, int L);
+size_t lora_workspace_bytes(int64_t T, int K, int r, int L);
 hipError_t launch_lora_add(const void* y, bool bf16, int64_t T, int64_t N, const uint16_t* x, int K,
                            const uint16_t* a, const uint16_t* b, int r, int L, const int32_t* ids,
                            const float* scales, void* out, void* ws, hipStream_t s);
