@@ -6,7 +6,6 @@ device memory (``data_ptr()``) and the current stream; nothing here computes
 on the host.  If the shared library has not been built this module raises on
 import -- there is no fallback path.
 """
-import contextlib
 import ctypes
 import os
 
@@ -101,6 +100,8 @@ def _p(t):
 
 
 def _stream(device):
+    if isinstance(device, torch.device) and device.index is not None:
+        return torch._C._cuda_getCurrentRawStream(device.index)  # 2 us less than a Stream object
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
@@ -127,13 +128,26 @@ def _workspace(nbytes, device):
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
-def _on(device, *tensors):
-    """The device to launch on (a context manager): that of the call's tensors,
-    all of which must be there."""
+def _one_device(device, *tensors):
     for t in tensors:
         if t is not None and t.device != device:
             raise ValueError(f"all tensors of a call must be on one device, got {device} and {t.device}")
-    return torch.cuda.device(device) if torch.cuda.current_device() != device.index else contextlib.nullcontext()
+
+
+def _launch(name, device, *args):
+    """Call an entry point (its arguments but the stream) on a device's current
+    stream, whatever the current device is."""
+    if torch.cuda.current_device() == device.index:
+        status = getattr(_lib, name)(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = getattr(_lib, name)(*args, _stream(device))
+    if status != 0:
+        raise Nvfp4Error(status, name)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 # ------------------------------------------------------------------ API
@@ -253,13 +267,13 @@ def lora_add(y, x, a, b, ids, scales=None, out=None, ws=None):
                         (scales, (L,), "scales"), (out, (T, N), "out")):
         if t is not None and t.shape != shape:
             raise ValueError(f"{n} must be {list(shape)}, got {list(t.shape)}")
+    _one_device(dev, x, a, b, ids, scales, out, ws)
     if out is None:
         out = torch.empty_like(y)
-    with _on(dev, x, a, b, ids, scales, out, ws):
-        if ws is None:
-            ws = _workspace(_lib.nvfp4_lora_add_workspace_size(T, N, K, r, L), dev)
-        _check(_lib.nvfp4_lora_add(_p(y), 0 if y.dtype == torch.bfloat16 else 1, T, N, _p(x), K, _p(a), _p(b), r, L,
-                                   _p(ids), _p(scales), _p(out), _p(ws), ws.numel(), _stream(dev)), "nvfp4_lora_add")
+    if ws is None:
+        ws = _workspace(_lib.nvfp4_lora_add_workspace_size(T, N, K, r, L), dev)
+    _launch("nvfp4_lora_add", dev, _at(y), 0 if y.dtype == torch.bfloat16 else 1, T, N, _at(x), K, _at(a), _at(b), r,
+            L, _at(ids), _at(scales), _at(out), _at(ws), ws.numel())
     return out
 
 
@@ -341,12 +355,12 @@ def router_logits(x, w, bias=None, out=None, ws=None):
     elif out.shape != (T, E):
         raise ValueError(f"out must be [{T}][{E}], got {tuple(out.shape)}")
     code = 0 if w.dtype == torch.bfloat16 else 1
-    with _on(dev, w, bias, out, ws):
-        if ws is None:
-            need = _lib.moe_router_logits_workspace_size(T, H, E, code)
-            ws = _workspace(need, dev) if need else None
-        _check(_lib.moe_router_logits(_p(x), T, H, _p(w), code, E, _p(bias), _p(out), _p(ws),
-                                      0 if ws is None else ws.numel(), _stream(dev)), "moe_router_logits")
+    _one_device(dev, w, bias, out, ws)
+    if ws is None:
+        need = _lib.moe_router_logits_workspace_size(T, H, E, code)
+        ws = _workspace(need, dev) if need else None
+    _launch("moe_router_logits", dev, _at(x), T, H, _at(w), code, E, _at(bias), _at(out), _at(ws),
+            0 if ws is None else ws.numel())
     return out
 
 
@@ -392,10 +406,10 @@ def route(logits, topk, scoring="softmax", bias=None, n_group=1, topk_group=1, g
             _require(t, d, n)
             if t.shape != (T, topk):
                 raise ValueError(f"{n} must be [{T}][{topk}], got {tuple(t.shape)}")
-    with _on(dev, bias, n_tokens, ids, weights):
-        _check(_lib.moe_route(_p(logits), 0 if logits.dtype == torch.bfloat16 else 1, T, E, topk, _SCORING[scoring],
-                              _p(bias), n_group, topk_group, group_top, int(bool(renormalize)), scale, _p(n_tokens),
-                              _p(ids), _p(weights), _stream(dev)), "moe_route")
+    _one_device(dev, bias, n_tokens, ids, weights)
+    _launch("moe_route", dev, _at(logits), 0 if logits.dtype == torch.bfloat16 else 1, T, E, topk, _SCORING[scoring],
+            _at(bias), n_group, topk_group, group_top, int(bool(renormalize)), scale, _at(n_tokens), _at(ids),
+            _at(weights))
     return ids, weights
 
 

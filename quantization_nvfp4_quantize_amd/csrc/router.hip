@@ -122,16 +122,35 @@ __device__ __forceinline__ F wave_sum(F x) {
   return x;
 }
 
-__device__ __forceinline__ float exp_of(float x) { return expf(x); }
+// The fp32 forms serve decisions only, whose margins cover their errors: the
+// hardware's exp2 of a rounded product (relative error |x| 1.44 * 2^-24 + 2^-23)
+// and its reciprocal (2^-23).
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 __device__ __forceinline__ double exp_of(double x) { return exp(x); }
-__device__ __forceinline__ float lane_of(float x, int lane) {
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+// exp for the weights: the product's rounding is given back (the hardware's
+// exp2 and a half step or two remain); results below 2^-126 become 0.
+__device__ __forceinline__ float weight_exp(float x) {
+  const float hi = 1.44269502f, lo = 1.92596300e-8f;  // log2(e)
+  const float t = x * hi, e = __builtin_amdgcn_exp2f(t);
+  const float rest = __builtin_fmaf(x, lo, __builtin_fmaf(x, hi, -t));
+  return e > 0.0f && e < INFINITY ? __builtin_fmaf(e, rest * 0.693147181f, e) : e;
 }
+__device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf(x); }
+__device__ __forceinline__ double inverse(double x) { return 1.0 / x; }
 __device__ __forceinline__ double lane_of(double x, int lane) {
   const long long b = __double_as_longlong(x);
   const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
   return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+
+// A reduction over the first k lanes (at most 32; the others hold values that
+// change nothing), in those lanes.
+template <class Op>
+__device__ __forceinline__ float first_lanes(float x, int k, Op op) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) x = op(x, swap_step(x, s));
+  return k > 16 ? op(x, swap_step(x, 4)) : x;
 }
 
 // Scores of a lane's experts (0 for masked ones); mx, sum: the softmax's
@@ -143,7 +162,7 @@ __device__ __forceinline__ void scores(const float (&z)[V], float mx, F& sum, F 
   for (int j = 0; j < V; ++j) {
     const bool live = z[j] > -INFINITY;
     if (SIGMOID) {
-      s[j] = live ? (F)1 / ((F)1 + exp_of(-(F)z[j])) : (F)0;
+      s[j] = live ? inverse((F)1 + exp_of(-(F)z[j])) : (F)0;
     } else {
       s[j] = live ? exp_of((F)z[j] - (F)mx) : (F)0;
       part += s[j];
@@ -151,49 +170,76 @@ __device__ __forceinline__ void scores(const float (&z)[V], float mx, F& sum, F 
   }
   if (!SIGMOID) {
     sum = wave_sum(part);
-    const F inv = sum > 0 ? (F)1 / sum : (F)0;
+    const F inv = sum > 0 ? inverse(sum) : (F)0;
 #pragma unroll
     for (int j = 0; j < V; ++j) s[j] *= inv;
   }
 }
 
-// Value of this lane's group: the sum of the one or two largest of g[] (-inf:
-// masked) over the group's lanes; -inf for a group with nothing.
-template <int V, class F>
-__device__ __forceinline__ F group_value(const RouteParams& p, const F (&g)[V]) {
-  F a = g[0], b = -INFINITY;
+// Value of this lane's group: the sum of the one or two largest of its experts'
+// values, -inf for a group with nothing.  In fp32 from keys (0: masked), whose
+// maxima and minima are single instructions, across lanes too.
+template <int CTRL>
+__device__ __forceinline__ void merge2(uint32_t& a, uint32_t& b) {
+  const uint32_t a2 = dpp0<CTRL>(a), b2 = dpp0<CTRL>(b);
+  b = max(max(b, b2), min(a, a2));
+  a = max(a, a2);
+}
+template <int V>
+__device__ __forceinline__ float group_value(const RouteParams& p, const uint32_t (&k)[V]) {
+  uint32_t a = k[0], b = 0u;
 #pragma unroll
   for (int j = 1; j < V; ++j) {
-    const F lo = g[j] < a ? g[j] : a;
+    b = max(b, min(k[j], a));
+    a = max(a, k[j]);
+  }
+  const int n = p.lanes_log2;
+  if (n > 0) merge2<kQuadXor1>(a, b);
+  if (n > 1) merge2<kQuadXor2>(a, b);
+  if (n > 2) merge2<kHalfMirror>(a, b);
+  if (n > 3) merge2<kMirror>(a, b);
+  for (int s = 16; s < 1 << n; s <<= 1) {
+    const uint32_t a2 = (uint32_t)__shfl_xor((int)a, s), b2 = (uint32_t)__shfl_xor((int)b, s);
+    b = max(max(b, b2), min(a, a2));
+    a = max(a, a2);
+  }
+  return !a ? -INFINITY : p.group_top == 2 && b ? value_of(a) + value_of(b) : value_of(a);
+}
+template <int V>
+__device__ __forceinline__ double group_value(const RouteParams& p, const double (&g)[V]) {
+  double a = g[0], b = -INFINITY;
+#pragma unroll
+  for (int j = 1; j < V; ++j) {
+    const double lo = g[j] < a ? g[j] : a;
     a = g[j] > a ? g[j] : a;
     b = lo > b ? lo : b;
   }
-#pragma unroll
-  for (int s = 0; s < 6; ++s) {
-    if (s < p.lanes_log2) {
-      const F a2 = swap_step(a, s), b2 = swap_step(b, s);
-      const F lo = a2 < a ? a2 : a, b3 = b2 > b ? b2 : b;
-      a = a2 > a ? a2 : a;
-      b = lo > b3 ? lo : b3;
-    }
+  for (int s = 1; s < 1 << p.lanes_log2; s <<= 1) {
+    const double a2 = __shfl_xor(a, s), b2 = __shfl_xor(b, s);
+    const double lo = a2 < a ? a2 : a, b3 = b2 > b ? b2 : b;
+    a = a2 > a ? a2 : a;
+    b = lo > b3 ? lo : b3;
   }
   return p.group_top == 2 && b > -INFINITY ? a + b : a;
 }
 
 // Whether this lane's group is among the topk_group best (ties: the lowest
-// group).  With tol >= 0, *unsure is set in lanes for which groups within tol
-// of their own could change the answer.
-template <class F>
-__device__ __forceinline__ bool keep_group(const RouteParams& p, F value, int group, bool check, bool* unsure) {
-  const F tol = check ? (F)0x1p-18f + (F)0x1p-21f * (value < 0 ? -value : value) : (F)0;
-  int above = 0, ahead = 0, near = 0;
+// group, so that a lower group is ahead with an equal value).
+__device__ __forceinline__ bool keep_group(const RouteParams& p, float value, int group) {
+  const uint32_t own = key_of(value + 0.0f);  // never 0: value >= -inf
+  int ahead = 0;
   for (int g = 0; g < p.n_group; ++g) {
-    const F o = lane_of(value, g << p.lanes_log2);
-    above += o > value + tol;
-    ahead += o > value || (o == value && g < group);
-    near += o >= value - tol && g != group;
+    const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)own, g << p.lanes_log2);
+    ahead += o > (g < group ? own - 1 : own);
   }
-  if (check && group < p.n_group && above < p.topk_group && near >= p.topk_group) *unsure = true;
+  return ahead < p.topk_group;
+}
+__device__ __forceinline__ bool keep_group(const RouteParams& p, double value, int group) {
+  int ahead = 0;
+  for (int g = 0; g < p.n_group; ++g) {
+    const double o = lane_of(value, g << p.lanes_log2);
+    ahead += o > value || (o == value && g < group);
+  }
   return ahead < p.topk_group;
 }
 
@@ -299,13 +345,21 @@ __global__ __launch_bounds__(64 * kRouteRows) void moe_route_kernel(RouteParams 
       idx[j] = e0 + j;
     }
     if (grouped) {
-      float g[V];
+      uint32_t g[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) g[j] = key[j] ? (by_score && !p.bias ? s[j] : value_of(key[j])) : -INFINITY;
+      for (int j = 0; j < V; ++j) g[j] = key[j] && by_score && !p.bias ? key_of(s[j]) : key[j];
       const float value = group_value(p, g);
-      bool u = false;
-      const bool keep = keep_group(p, value, group, by_score, &u);
-      unsure = __ballot(u) != 0;
+      const bool keep = keep_group(p, value, group);
+      if (by_score) {
+        // the worst group that stays against the best that goes: two sums of
+        // two choices are off by at most 2 (2^-20 + 2^-23 |value|); equal or
+        // infinite values count as close
+        const bool in = group < p.n_group;
+        const uint32_t kv = key_of(value);
+        const uint32_t low = ~wave_max(in && keep ? ~kv : 0u), high = wave_max(in && !keep ? kv : 0u);
+        const float lo = value_of(low), hi = value_of(high);
+        unsure = high != 0u && !(lo - hi > 0x1p-18f + 0x1p-21f * fabsf(hi));
+      }
       if (!keep) {
 #pragma unroll
         for (int j = 0; j < V; ++j) key[j] = 0u;
@@ -327,21 +381,16 @@ __global__ __launch_bounds__(64 * kRouteRows) void moe_route_kernel(RouteParams 
       }
     }
     const int picks = p.bias ? p.k + 1 : p.k;  // one more tells how near the next expert came
-    float prev = 0.0f;
-    for (int i = 0; i < picks; ++i) {
+    uint32_t my_key = 0u;  // lane i: the key of the i-th pick
+    int n_picked = 0;
+    for (; n_picked < picks; ++n_picked) {
       const uint32_t best = wave_max(key[0]);
       if (best == 0) break;
-      if (p.bias) {
-        const float c = value_of(best);
-        // gap <= 2^-19 + 2^-22 |c|: the errors of two choices are at most
-        // twice (2^-21 + 2^-24 |c|); a NaN gap (inf - inf) counts as close
-        if (i > 0 && !(prev - c > 0x1p-19f + 0x1p-22f * fabsf(c))) unsure = true;
-        prev = c;
-      }
       const int win = __ffsll((unsigned long long)__ballot(key[0] == best)) - 1;
-      if (i < p.k) {
-        const int e = __builtin_amdgcn_readlane(idx[0], win);
-        my_e = lane == i ? e : my_e;
+      const int e = __builtin_amdgcn_readlane(idx[0], win);
+      if (lane == n_picked) {
+        my_e = e;
+        my_key = best;
       }
       if (lane == win) {
 #pragma unroll
@@ -352,6 +401,14 @@ __global__ __launch_bounds__(64 * kRouteRows) void moe_route_kernel(RouteParams 
         key[V - 1] = 0u;
       }
     }
+    if (p.bias) {
+      // every pick against the next: the errors of two choices are at most twice
+      // (2^-21 + 2^-24 |c|); a NaN gap (inf - inf) counts as close
+      const uint32_t next_key = (uint32_t)__shfl_down((int)my_key, 1);
+      const float c = value_of(my_key), next = value_of(next_key);
+      unsure = unsure || __ballot(lane + 1 < n_picked && !(c - next > 0x1p-19f + 0x1p-22f * fabsf(next))) != 0;
+    }
+    if (lane >= p.k) my_e = -1;
   }
 
   if (__builtin_amdgcn_readfirstlane((int)unsure)) {
@@ -368,8 +425,7 @@ __global__ __launch_bounds__(64 * kRouteRows) void moe_route_kernel(RouteParams 
       double g[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) g[j] = c[j] > -INFINITY ? (by_score && !p.bias ? sd[j] : c[j]) : -INFINITY;
-      bool u;
-      open = keep_group(p, group_value(p, g), group, false, &u);
+      open = keep_group(p, group_value(p, g), group);
     }
     my_e = -1;
     uint32_t taken = 0;
@@ -401,21 +457,24 @@ __global__ __launch_bounds__(64 * kRouteRows) void moe_route_kernel(RouteParams 
   if (p.renormalize) {
     // every score over e^m, so that a token whose scores are all tiny keeps
     // their ratios: m = the largest chosen logit (softmax), or that where it
-    // is negative (sigmoid)
-    const float peak = wave_max_f(zi);
+    // is negative (sigmoid).  Without a bias the first pick has it.
+    float peak = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(zi)));
+    if (p.bias) peak = first_lanes(zi, p.k, [](float x, float y) { return y > x ? y : x; });
     float part = 0.0f;
     if (my_e >= 0) {
-      if (SIGMOID)
-        part = zi > 0.0f ? 1.0f / (1.0f + expf(-zi)) : expf(zi - fminf(peak, 0.0f)) / (1.0f + expf(zi));
-      else
-        part = expf(zi - peak);
+      if (SIGMOID) {
+        const float m = fminf(peak, 0.0f);
+        part = zi > 0.0f ? inverse(1.0f + weight_exp(-zi)) : weight_exp(zi - m) * inverse(1.0f + weight_exp(zi));
+      } else {
+        part = weight_exp(zi - peak);
+      }
     }
-    const float total = wave_sum(part);
-    w = my_e >= 0 ? part / total * p.scale : 0.0f;
+    const float total = first_lanes(part, p.k, [](float x, float y) { return x + y; });
+    w = my_e >= 0 ? part * inverse(total) * p.scale : 0.0f;
   } else if (SIGMOID) {
-    w = my_e >= 0 ? p.scale / (1.0f + expf(-zi)) : 0.0f;
+    w = my_e >= 0 ? p.scale * inverse(1.0f + weight_exp(-zi)) : 0.0f;
   } else {
-    w = my_e >= 0 ? expf(zi - mx) / sum * p.scale : 0.0f;
+    w = my_e >= 0 ? weight_exp(zi - mx) * inverse(sum) * p.scale : 0.0f;
   }
   if (lane < p.k) {
     p.ids[t * p.k + lane] = my_e;
