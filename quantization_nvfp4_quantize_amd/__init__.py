@@ -128,9 +128,16 @@ def _workspace(nbytes, device):
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
-def _one_device(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
+def _require_all(device, *specs):
+    """Each (tensor or None, dtype, shape, name) on the device and contiguous:
+    _require in one pass over the tensors of a short call."""
+    for t, dtype, shape, name in specs:
+        if t is None:
+            continue
+        if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_cuda or not t.is_contiguous():
+            _require(t, dtype, name)
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
             raise ValueError(f"all tensors of a call must be on one device, got {device} and {t.device}")
 
 
@@ -257,17 +264,14 @@ def lora_add(y, x, a, b, ids, scales=None, out=None, ws=None):
     run at the same time."""
     if y.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"y must be bfloat16 or float32, got {y.dtype}")
-    for t, d, n in ((y, y.dtype, "y"), (x, torch.bfloat16, "x"), (a, torch.bfloat16, "a"), (b, torch.bfloat16, "b"),
-                    (ids, torch.int32, "ids"), (scales, torch.float32, "scales"), (out, y.dtype, "out")):
-        _require(t, d, n)
-    if y.dim() != 2 or x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+    if y.dim() != 2 or x.dim() != 2 or a.dim() != 3:
         raise ValueError("y and x must be matrices, a [L][r][K] and b [L][N][r]")
     (T, N), K, (L, r, _), dev = y.shape, x.shape[1], a.shape, y.device
-    for t, shape, n in ((x, (T, K), "x"), (a, (L, r, K), "a"), (b, (L, N, r), "b"), (ids, (T,), "ids"),
-                        (scales, (L,), "scales"), (out, (T, N), "out")):
-        if t is not None and t.shape != shape:
-            raise ValueError(f"{n} must be {list(shape)}, got {list(t.shape)}")
-    _one_device(dev, x, a, b, ids, scales, out, ws)
+    _require_all(dev, (y, y.dtype, (T, N), "y"), (x, torch.bfloat16, (T, K), "x"),
+                 (a, torch.bfloat16, (L, r, K), "a"), (b, torch.bfloat16, (L, N, r), "b"),
+                 (ids, torch.int32, (T,), "ids"), (scales, torch.float32, (L,), "scales"), (out, y.dtype, (T, N), "out"))
+    if ws is not None and ws.device != dev:
+        raise ValueError(f"ws must be on {dev}")
     if out is None:
         out = torch.empty_like(y)
     if ws is None:
@@ -339,23 +343,18 @@ def router_logits(x, w, bias=None, out=None, ws=None):
     """The router's gate projection: float32 logits [T][E] = x @ w^T (+ bias).
     x bf16 [T][H] (H % 32 == 0); w [E][H] bf16 or float32 (all its bits are
     used); bias float32 [E]."""
-    _require(x, torch.bfloat16, "x")
     if w.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"w must be bfloat16 or float32, got {w.dtype}")
-    _require(w, w.dtype, "w")
-    _require(bias, torch.float32, "bias")
-    _require(out, torch.float32, "out")
-    if x.dim() != 2 or w.dim() != 2 or w.shape[1] != x.shape[1]:
+    if x.dim() != 2 or w.dim() != 2:
         raise ValueError(f"x must be [T][H] and w [E][H], got {tuple(x.shape)} and {tuple(w.shape)}")
     (T, H), E, dev = x.shape, w.shape[0], x.device
-    if bias is not None and bias.shape != (E,):
-        raise ValueError(f"bias must be [{E}], got {tuple(bias.shape)}")
+    _require_all(dev, (x, torch.bfloat16, (T, H), "x"), (w, w.dtype, (E, H), "w"), (bias, torch.float32, (E,), "bias"),
+                 (out, torch.float32, (T, E), "out"))
+    if ws is not None and ws.device != dev:
+        raise ValueError(f"ws must be on {dev}")
     if out is None:
         out = torch.empty((T, E), dtype=torch.float32, device=dev)
-    elif out.shape != (T, E):
-        raise ValueError(f"out must be [{T}][{E}], got {tuple(out.shape)}")
     code = 0 if w.dtype == torch.bfloat16 else 1
-    _one_device(dev, w, bias, out, ws)
     if ws is None:
         need = _lib.moe_router_logits_workspace_size(T, H, E, code)
         ws = _workspace(need, dev) if need else None
@@ -384,29 +383,18 @@ def route(logits, topk, scoring="softmax", bias=None, n_group=1, topk_group=1, g
     out: (ids, weights) to fill."""
     if logits.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"logits must be bfloat16 or float32, got {logits.dtype}")
-    _require(logits, logits.dtype, "logits")
     if logits.dim() != 2:
         raise ValueError("logits must be [T][E]")
-    T, E = logits.shape
     if scoring not in _SCORING:
         raise ValueError(f"scoring must be one of {sorted(_SCORING)}, got {scoring!r}")
-    _require(bias, torch.float32, "bias")
-    if bias is not None and bias.shape != (E,):
-        raise ValueError(f"bias must be [{E}], got {tuple(bias.shape)}")
-    _require(n_tokens, torch.int32, "n_tokens")
-    if n_tokens is not None and n_tokens.numel() != 1:
-        raise ValueError("n_tokens must hold one value")
-    dev = logits.device
+    (T, E), dev = logits.shape, logits.device
     if out is None:
-        ids = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=dev)
-        weights = torch.empty((T, max(topk, 0)), dtype=torch.float32, device=dev)
-    else:
-        ids, weights = out
-        for t, d, n in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
-            _require(t, d, n)
-            if t.shape != (T, topk):
-                raise ValueError(f"{n} must be [{T}][{topk}], got {tuple(t.shape)}")
-    _one_device(dev, bias, n_tokens, ids, weights)
+        shape = (T, max(topk, 0))
+        out = (torch.empty(shape, dtype=torch.int32, device=dev), torch.empty(shape, dtype=torch.float32, device=dev))
+    ids, weights = out
+    _require_all(dev, (logits, logits.dtype, (T, E), "logits"), (bias, torch.float32, (E,), "bias"),
+                 (n_tokens, torch.int32, (1,), "n_tokens"), (ids, torch.int32, (T, max(topk, 0)), "ids"),
+                 (weights, torch.float32, (T, max(topk, 0)), "weights"))
     _launch("moe_route", dev, _at(logits), 0 if logits.dtype == torch.bfloat16 else 1, T, E, topk, _SCORING[scoring],
             _at(bias), n_group, topk_group, group_top, int(bool(renormalize)), scale, _at(n_tokens), _at(ids),
             _at(weights))

@@ -272,14 +272,17 @@ __global__ __launch_bounds__(256) void lora_down_tile_kernel(LoraParams p) {
 // Groups up to kGroupTokens tokens by adapter, one workgroup of 1024 threads:
 // a histogram in LDS, a scan, and each token's place from a second count.  The
 // places inside an adapter depend on the order of the atomics, which changes
-// no result.  Tokens without an adapter come last, in tiles of expert -1.
+// no result.  Tokens without an adapter come last, in tiles of expert -1.  The
+// ids are requested four at a time and kept in LDS for the second count: the
+// kernel lasts as long as its loads.
 __global__ __launch_bounds__(1024) void lora_group_kernel(LoraParams p) {
   __shared__ int count[513], place[513], wsum[16];
+  __shared__ uint16_t adapter[kGroupTokens];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, T = (int)p.T;
   if (tid <= p.L) count[tid] = 0;
   __syncthreads();
   // one count per wave where its 64 tokens share an adapter
-  auto add = [&](int* c, int id, int n) {
+  auto add = [&](int* c, int id) {
     const int first = __builtin_amdgcn_readfirstlane(id);
     if (__ballot(id != first) == 0) {
       const uint64_t all = __ballot(true);
@@ -287,13 +290,21 @@ __global__ __launch_bounds__(1024) void lora_group_kernel(LoraParams p) {
       if (lane == 0) base = atomicAdd(&c[first], __popcll(all));
       return __builtin_amdgcn_readfirstlane(base) + lane;
     }
-    return atomicAdd(&c[id], n);
+    return atomicAdd(&c[id], 1);
   };
-  auto id_of = [&](int t) {
-    const int id = p.ids[t];
-    return id < 0 || id >= p.L ? p.L : id;
-  };
-  for (int t = tid; t < T; t += 1024) add(count, id_of(t), 1);
+  for (int t0 = tid; t0 < T; t0 += 4 * 1024) {
+    int id[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) id[i] = p.ids[min(t0 + 1024 * i, T - 1)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + 1024 * i;
+      if (t >= T) break;
+      const int e = id[i] < 0 || id[i] >= p.L ? p.L : id[i];
+      adapter[t] = (uint16_t)e;
+      add(count, e);
+    }
+  }
   __syncthreads();
   // tokens (low half) and tiles (high half) of the adapters before this one
   const int n = tid <= p.L ? count[tid] : 0, tiles = (n + p.tile_rows - 1) / p.tile_rows;
@@ -316,7 +327,7 @@ __global__ __launch_bounds__(1024) void lora_group_kernel(LoraParams p) {
     if (tid == p.L) *p.ntiles = first + tiles;
   }
   __syncthreads();
-  for (int t = tid; t < T; t += 1024) p.perm[add(place, id_of(t), 1)] = t;
+  for (int t = tid; t < T; t += 1024) p.perm[add(place, adapter[t])] = t;
 }
 
 // Eight fp32 values -> TERMS bf16 fragments that add up to them.

@@ -352,13 +352,21 @@ __global__ __launch_bounds__(64 * kRouteRows) void moe_route_kernel(RouteParams 
       const bool keep = keep_group(p, value, group);
       if (by_score) {
         // the worst group that stays against the best that goes: two sums of
-        // two choices are off by at most 2 (2^-20 + 2^-23 |value|); equal or
-        // infinite values count as close
+        // two choices c, each off by at most 2^-20 + 2^-24 |c|, and rounded;
+        // equal or infinite values count as close.  Scores are at most 1; with
+        // a bias the largest |c| bounds the errors (a sum may be small where
+        // its terms are not).
         const bool in = group < p.n_group;
         const uint32_t kv = key_of(value);
         const uint32_t low = ~wave_max(in && keep ? ~kv : 0u), high = wave_max(in && !keep ? kv : 0u);
-        const float lo = value_of(low), hi = value_of(high);
-        unsure = high != 0u && !(lo - hi > 0x1p-18f + 0x1p-21f * fabsf(hi));
+        float most = 1.0f;
+        if (p.bias) {
+          uint32_t m = 0u;
+#pragma unroll
+          for (int j = 0; j < V; ++j) m = max(m, key[j] ? __float_as_uint(value_of(key[j])) & 0x7fffffffu : 0u);
+          most = __uint_as_float(wave_max(m));
+        }
+        unsure = high != 0u && !(value_of(low) - value_of(high) > 0x1p-18f + 0x1p-21f * most);
       }
       if (!keep) {
 #pragma unroll
@@ -402,8 +410,9 @@ __global__ __launch_bounds__(64 * kRouteRows) void moe_route_kernel(RouteParams 
       }
     }
     if (p.bias) {
-      // every pick against the next: the errors of two choices are at most twice
-      // (2^-21 + 2^-24 |c|); a NaN gap (inf - inf) counts as close
+      // every pick against the next: a choice is off by at most 2^-20 (the score's
+      // exponentials and sum) + 2^-24 |c| (its own rounding), two of them by twice
+      // that; a NaN gap (inf - inf) counts as close
       const uint32_t next_key = (uint32_t)__shfl_down((int)my_key, 1);
       const float c = value_of(my_key), next = value_of(next_key);
       unsure = unsure || __ballot(lane + 1 < n_picked && !(c - next > 0x1p-19f + 0x1p-22f * fabsf(next))) != 0;
@@ -520,6 +529,7 @@ hipError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, con
   p.ids = ids;
   p.w = w;
   // whole-lane vector loads: every lane's v experts are there and aligned
+  if (p.v > 16) return hipErrorInvalidValue;  // never for n_group <= 64 and E <= 512
   const bool vec = p.S % p.v == 0 && E % p.v == 0 && (p.v == 2 || p.v == 4);
   if (p.v == 1) return route_go<1, false>(p, bf16, sigmoid, s);
   if (p.v == 2) return vec ? route_go<2, true>(p, bf16, sigmoid, s) : route_go<2, false>(p, bf16, sigmoid, s);

@@ -81,7 +81,8 @@ def _check(out, y, x, a, b, ids, s):
 SHAPES = [(1, 32, 8, 8, 1), (1, 7168, 2048, 16, 4), (2, 64, 24, 16, 2), (15, 96, 72, 24, 3), (16, 160, 264, 32, 5),
           (17, 1280, 256, 40, 2), (65, 512, 1000, 64, 40), (100, 768, 512, 128, 7), (300, 256, 136, 96, 512),
           (1000, 128, 96, 8, 9), (1024, 64, 64, 16, 64), (1025, 64, 320, 48, 6), (1500, 512, 264, 16, 3),
-          (4097, 96, 40, 56, 33), (5003, 256, 128, 64, 5)]
+          (4097, 96, 40, 56, 33), (5003, 256, 128, 64, 5), (256, 2048, 96, 32, 3), (257, 1024, 48, 128, 2),
+          (500, 4096, 40, 16, 20), (513, 512, 600, 104, 1)]
 
 
 @pytest.mark.parametrize("T,K,N,r,L", SHAPES)
@@ -98,11 +99,22 @@ def test_lora_shapes(nv, T, K, N, r, L, dtype):
         _check(out, *p)
 
 
-@pytest.mark.parametrize("T", [1, 40, 1024, 2100])
+@pytest.mark.parametrize("T", [1, 40, 256, 257, 1024, 2100])
 @pytest.mark.parametrize("kind", ["one", "none", "requests", "distinct", "mixed"])
 def test_lora_ids(nv, T, kind):
     p = _problem(T, 128, 200, 16, 37, BF, kind, T)
     _check(nv.lora_add(*p[:5], scales=p[5]), *p)
+
+
+@pytest.mark.parametrize("T,K,L", [(16384, 64, 512), (16384, 64, 3), (16385, 64, 5), (17000, 96, 512)])
+@pytest.mark.parametrize("kind", ["one", "requests", "mixed"])
+def test_lora_many_tokens(nv, T, K, L, kind):
+    """The groupings of one and of many workgroups at their border."""
+    p = _problem(T, K, 16, 8, L, BF, kind, T + L)
+    _check(nv.lora_add(*p[:5], scales=p[5]), *p)
+    y = p[0].clone()
+    nv.lora_add(y, *p[1:5], scales=p[5], out=y)
+    assert torch.equal(y, nv.lora_add(*p[:5], scales=p[5]))
 
 
 @pytest.mark.parametrize("dtype", [BF, torch.float32])

@@ -146,6 +146,20 @@ def test_route_decides_between_neighbouring_groups(nv, scoring):
     _check(nv, z, 8, scoring=scoring, n_group=G, topk_group=4, group_top=2)
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_groups_with_large_opposite_biases(nv, scoring):
+    """A group's value may be small where its terms are large: what their
+    roundings leave decides then, not the sum's size."""
+    E, G = 64, 8
+    z = _logits(40, E, 12)
+    b = torch.full((E,), -INF, device=DEV)
+    for g in range(G):               # two experts a group, 1e6 up and down: fp32 sums lose the scores
+        b[8 * g + g], b[8 * g + (g + 3) % 8] = 1.0e6, -1.0e6
+    _check(nv, z, 2, bias=b, scoring=scoring, n_group=G, topk_group=3, group_top=2)
+    b = torch.where(b > 0, b - 0.75, b)
+    _check(nv, z, 4, bias=b, scoring=scoring, n_group=G, topk_group=2, group_top=2)
+
+
 def test_route_large_batch(nv):
     """Many tokens, against torch in 64 bits (values without ties)."""
     T, E, k = 40001, 256, 8
@@ -271,7 +285,8 @@ def _gate_check(y, x, w, bias):
 
 GATE_SHAPES = [(1, 32, 1), (1, 7168, 256), (3, 64, 5), (16, 256, 8), (17, 96, 17), (33, 1280, 160), (100, 512, 511),
                (129, 2048, 72), (130, 7168, 256), (300, 160, 512), (1000, 768, 40), (513, 1024, 128),
-               (2049, 480, 200), (4100, 256, 256)]
+               (2049, 480, 200), (4100, 256, 256), (8, 2048, 33), (9, 2048, 33), (256, 640, 511), (257, 640, 512),
+               (16, 7168, 8), (700, 4096, 72), (2000, 4096, 130)]
 
 
 @pytest.mark.parametrize("T,H,E", GATE_SHAPES)
