@@ -37,6 +37,11 @@ __device__ __forceinline__ f32x16 mfma32(uint4 a, uint4 b, f32x16 c) {
                                                  0, 0);
 }
 
+__device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                 0, 0);
+}
+
 __device__ __forceinline__ void store_logit(const GateParams& p, int part, int64_t t, int e, float v) {
   if (t < p.T && e < p.E) p.out[((int64_t)part * p.T + t) * p.E + e] = p.parts == 1 && p.bias ? v + p.bias[e] : v;
 }
@@ -73,7 +78,7 @@ constexpr int kDotTokens = 8;
 
 template <bool F32W, int NT>
 __global__ __launch_bounds__(kDotThreads) void gate_dot_kernel(GateParams p) {
-  constexpr int kUnroll = NT <= 4 ? 4 : 2;
+  constexpr int kUnroll = NT <= 2 ? 4 : 1;
   __shared__ float part[kDotThreads / 64][NT];
   const int e = blockIdx.x, tid = threadIdx.x, chunks = p.H / 8;
   float acc[NT];
@@ -138,63 +143,93 @@ __global__ __launch_bounds__(kDotThreads) void gate_dot_kernel(GateParams p) {
 
 // ---- few tokens: 32 tokens x 32 experts and a slice of K per workgroup, a
 // quarter of the slice per wave, operands straight from memory into
-// registers.  A call of this size lasts about as long as its longest chain of
-// loads, so the slices are short: a wave has its whole share in flight at once
-// where K allows.  Workgroups that run on one XCD (blockIdx % 8) take the same
-// slices, so an XCD's L2 fetches its part of x and w and not all of both.
+// registers.  2 x 2 MFMA tiles of 16 x 16, whose loads take 64 bytes of 16 rows
+// each.  Workgroups that run on one XCD (blockIdx % 8) take the same slices, so
+// an XCD's L2 fetches its part of x and w and not all of both.  The loop is
+// short: such a call spends most of its time on trips to memory, and fetching
+// its code is one of them.  Batches of 8, 4, 2 and 1 steps of loads take 8.3,
+// 6.5, 5.7 and 5.6 us for T256 H2048 E64, 8.7, 8.7, 8.1 and 8.0 for T128 H7168
+// E256 with operands in the caches; two keep more in flight from memory.
 constexpr int kSliceWaves = 4;
 constexpr int kSliceTile = 32;
 
 template <bool F32W>
 __global__ __launch_bounds__(64 * kSliceWaves) void gate_slice_kernel(GateParams p) {
-  constexpr int kSteps = F32W ? 8 : 16;  // K steps of 16 in flight
+  constexpr int kSteps = 2;  // K steps of 32 per batch of loads
   __shared__ float part[kSliceWaves][32 * 33];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int etiles = (p.E + kSliceTile - 1) / kSliceTile;
   const int slice = blockIdx.x % p.slices, tile = blockIdx.x / p.slices;
   const int e0 = tile % etiles * kSliceTile;
   const int64_t t0 = (int64_t)(tile / etiles) * kSliceTile;
-  const int r = lane & 31, g = lane >> 5;
-  const uint16_t* xr = p.x + min(t0 + r, p.T - 1) * p.H + 8 * g;
-  const int64_t wo = (int64_t)min(e0 + r, p.E - 1) * p.H + 8 * g;
-  const int nk = p.H / 16, share = p.slices * kSliceWaves, mine = slice * kSliceWaves + wave;
+  const int r = lane & 15, g = lane >> 4;
+  const uint16_t* xr[2];
+  int64_t wo[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    xr[h] = p.x + min(t0 + 16 * h + r, p.T - 1) * p.H + 8 * g;
+    wo[h] = (int64_t)min(e0 + 16 * h + r, p.E - 1) * p.H + 8 * g;
+  }
+  const int nk = p.H / 32, share = p.slices * kSliceWaves, mine = slice * kSliceWaves + wave;
   const int k0 = (int)((uint32_t)(nk * mine) / (uint32_t)share), k1 = (int)((uint32_t)(nk * (mine + 1)) / (uint32_t)share);
-  f32x16 acc = {};
+  f32x4 acc[2][2] = {};  // [token half][expert half]
   for (int k = k0; k < k1; k += kSteps) {
-    uint4 a[kSteps];
+    uint4 a[kSteps][2];
     if constexpr (F32W) {
-      float4 b[kSteps][2];
+      float4 b[kSteps][2][2];
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const int kk = 16 * min(k + i, k1 - 1);
-        a[i] = *reinterpret_cast<const uint4*>(xr + kk);
-        const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p.w) + wo + kk);
-        b[i][0] = s[0];
-        b[i][1] = s[1];
+        const int kk = 32 * min(k + i, k1 - 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          a[i][h] = *reinterpret_cast<const uint4*>(xr[h] + kk);
+          const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p.w) + wo[h] + kk);
+          b[i][h][0] = s[0];
+          b[i][h][1] = s[1];
+        }
       }
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
         if (k + i < k1) {
-          const Split3 s = split3(b[i][0], b[i][1]);
 #pragma unroll
-          for (int q = 2; q >= 0; --q) acc = mfma32(a[i], s.f[q], acc);
+          for (int e = 0; e < 2; ++e) {
+            const Split3 s = split3(b[i][e][0], b[i][e][1]);
+#pragma unroll
+            for (int q = 2; q >= 0; --q)
+#pragma unroll
+              for (int t = 0; t < 2; ++t) acc[t][e] = mfma16(a[i][t], s.f[q], acc[t][e]);
+          }
         }
       }
     } else {
-      uint4 b[kSteps];
+      uint4 b[kSteps][2];
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const int kk = 16 * min(k + i, k1 - 1);
-        a[i] = *reinterpret_cast<const uint4*>(xr + kk);
-        b[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.w) + wo + kk);
+        const int kk = 32 * min(k + i, k1 - 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          a[i][h] = *reinterpret_cast<const uint4*>(xr[h] + kk);
+          b[i][h] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.w) + wo[h] + kk);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i)
-        if (k + i < k1) acc = mfma32(a[i], b[i], acc);
+      for (int i = 0; i < kSteps; ++i) {
+        if (k + i < k1) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) acc[t][e] = mfma16(a[i][t], b[i][e], acc[t][e]);
+        }
+      }
     }
   }
+  // accumulator element i: token 4 g + i, expert lane % 16 of its tile
 #pragma unroll
-  for (int i = 0; i < 16; ++i) part[wave][33 * acc_row(i, lane) + r] = acc[i];
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[wave][33 * (16 * t + 4 * g + i) + 16 * e + r] = acc[t][e][i];
   __syncthreads();
   for (int i = threadIdx.x; i < 32 * 32; i += 64 * kSliceWaves) {
     const int row = i >> 5, col = i & 31;
@@ -390,12 +425,13 @@ __global__ __launch_bounds__(256) void gate_sum_kernel(const float* __restrict__
   }
 }
 
-// Which kernel takes a call, and its workspace.  Measured (us, bf16 H7168
-// E256 unless said otherwise): dot against slices at 8 tokens 6.0 / 8.0, at 12
-// 9.4 / 8.2; slices against tiles at 256 tokens 12.8 / 14.2, at 512 20.7 / 14.9;
-// fp32 weights, whose tiles cost three times as much, by the work of the
-// slices: H7168 E256 at 256 tokens 17.2 / 23.7, at 512 28.3 / 24.7; H4096 E72 at
-// 1024 tokens 13.2 / 18.8; H2048 E64 at 2048 tokens 12.1 / 17.4.
+// Which kernel takes a call, and its workspace.  Measured (us of GPU time):
+// dot against slices (H7168 E256) at 8 tokens 5.9 / 6.7, at 12 tokens 9.4 / 6.4
+// (with 16 tokens per workgroup); slices against tiles by the slices' work,
+// small tiles x H: bf16 H7168 E256 at 256 tokens (0.46 M) 11.7 / 14.0, at 300
+// (0.57 M) 14.8 / 13.9; H4096 E72 at 1024 (0.39 M) 10.6 / 12.2, at 2048 (0.79 M)
+// 16.8 / 13.2; fp32, whose tiles cost three times as much, H7168 E256 at 384 (0.69
+// M) 20.1 / 23.1, at 512 (0.92 M) 24.7 / 22.6, H4096 E72 at 2048 21.6 / 20.8.
 struct GatePlan {
   enum Kind { kDot, kSlice, kTile } kind;
   int slices, parts;
@@ -407,9 +443,9 @@ GatePlan gate_plan(int64_t T, int64_t H, int64_t E, bool w_bf16) {
   if (T <= kDotTokens) return g;
   const int64_t big = (T + kTileRows - 1) / kTileRows * ((E + kTileRows - 1) / kTileRows);
   const int64_t small = (T + kSliceTile - 1) / kSliceTile * ((E + kSliceTile - 1) / kSliceTile);
-  if (H % 64 != 0 || (w_bf16 ? T <= 256 : small * H <= 1 << 19)) {
+  if (H % 64 != 0 || small * H <= (w_bf16 ? 1 << 19 : 11 << 16)) {
     g.kind = GatePlan::kSlice;
-    // about a workgroup per CU and four K steps of 16 or more per wave;
+    // about a workgroup per CU and two K steps of 32 or more per wave;
     // multiples of the 8 XCDs, or with a short K a power of two
     const int64_t want = std::min<int64_t>((256 + small - 1) / small, H / 16 / (4 * kSliceWaves));
     if (want >= 8)
