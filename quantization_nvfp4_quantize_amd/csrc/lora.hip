@@ -362,10 +362,10 @@ __device__ __forceinline__ Terms<TERMS> split(const f32x4& a, const f32x4& b) {
 // (token l % 16, g = l / 16) ends with columns col_of(q, 4 g + i) of its token in
 // element i of accumulator q, 16 bytes at a time, and the four g of a token with
 // 64 adjacent bytes per access; an adapter's rows of b are loaded once for the
-// tile.  Bound by y and out: 62 us of the 81 for 4096 tokens, N 16384, r 32, bf16
-// are this kernel's, 268 MB at 4.3 TB/s.  Tiles of tokens without an adapter go
-// the same way without a product (a loop token by token over them, 11 tiles
-// of the 75, took 70 us longer than all the others).  Workgroups of one tile are
+// tile.  Bound by y and out: 64 us of the 80 for 4096 tokens, N 16384, r 32, bf16
+// are this kernel's, 268 MB at 4.2 TB/s.  Tiles of tokens without an adapter go
+// the same way without a product (a loop token by token over them, 11 tiles of
+// the 75, took 70 us longer than all the others).  Workgroups of one tile are
 // launched next to each other: launched tile by tile within a chunk the same
 // call takes 5 us more, in runs of tiles per XCD 6 us more.
 constexpr int kUpWaves = 4;
@@ -390,106 +390,130 @@ __device__ __forceinline__ uint4 add_bf16(const uint4& v, const f32x4& lo, const
   return __builtin_bit_cast(uint4, r);
 }
 
-// RC: 32-wide chunks of r; MT: MFMA tiles of 16 tokens per tile.
+// RC: 32-wide chunks of r; MT: MFMA tiles of 16 tokens per tile.  Columns and
+// offsets inside an adapter fit 32 bits (N <= 2^20, r <= 128).
 template <bool BF16, int RC, int MT>
-__global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraParams p) {
+__device__ __forceinline__ void lora_up(const LoraParams& p) {
   constexpr int TERMS = BF16 ? 2 : 3;
-  constexpr int VEC = BF16 ? 1 : 2;  // 16-byte loads per eight columns
+  constexpr int kSize = BF16 ? 2 : 4;
+  constexpr int PIECES = BF16 ? 2 : 4;  // 16-byte accesses of a lane per token and chunk, 64 bytes apart
   __shared__ uint4 us[MT * RC * TERMS][64];
   if (p.ntiles && (int)blockIdx.y >= *p.ntiles) return;
   const GemmTile tile = p.tiles[blockIdx.y];
   if (tile.nrows == 0) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
-  const int64_t n_first = ((int64_t)blockIdx.x * kUpWaves + wave) * 64;
-  const int64_t n_step = (int64_t)gridDim.x * kUpWaves * 64;
-  constexpr int kSize = BF16 ? 2 : 4;
+  const int N = (int)p.N, r = p.r;
+  const int n_first = ((int)blockIdx.x * kUpWaves + wave) * 64, n_step = (int)gridDim.x * kUpWaves * 64;
   const bool bare = tile.expert < 0;  // tokens without an adapter: out = y
   if (bare && p.out == p.y) return;
-  int64_t row[MT];
+  int64_t row[MT];  // byte offset of this lane's token
 #pragma unroll
-  for (int i = 0; i < MT; ++i) row[i] = p.perm[tile.row0 + min(16 * i + m, tile.nrows - 1)];
-  constexpr int PIECES = BF16 ? 2 : 4;  // 16-byte accesses of a lane per token, 64 bytes apart
-  uint4 y[MT][PIECES], bf[RC][4];
-  auto load = [&](int64_t n) {
-    const int64_t nl = n + 16 / kSize * g;
+  for (int i = 0; i < MT; ++i)
+    row[i] = p.perm[tile.row0 + min(16 * i + m, tile.nrows - 1)] * (p.N * kSize) + 16 * g;
+  const char* const yb = static_cast<const char*>(p.y);
+  char* const ob = static_cast<char*>(p.out);
+  // 16 bytes of y from byte 64 h of the chunk at column n on; past the end of
+  // the row (whole pieces, N % 8 == 0) the last ones again
+  auto load_y = [&](int i, int h, int n) {
+    const int at = min(n * kSize + 64 * h, N * kSize - 16 - 16 * g);
+    return *reinterpret_cast<const uint4*>(yb + row[i] + at);
+  };
+  auto inside = [&](int h, int n) { return n * kSize + 64 * h + 16 * g < N * kSize; };
+  if (bare) {
+    for (int n = n_first; n < N; n += n_step) {
+      uint4 y[MT][PIECES];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if (16 * i < tile.nrows) {
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < PIECES; ++h) y[i][h] = load_y(i, h, n);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int h = 0; h < PIECES; ++h)
-          y[i][h] = *reinterpret_cast<const uint4*>(
-              static_cast<const char*>(p.y) + (row[i] * p.N + min(nl + 64 / kSize * h, p.N - 16 / kSize)) * kSize);
+          if (16 * i + m < tile.nrows && inside(h, n))
+            *reinterpret_cast<uint4*>(ob + row[i] + n * kSize + 64 * h) = y[i][h];
+    }
+    return;
+  }
+  for (int w = wave; w < MT * RC; w += kUpWaves) {
+    const int i = w / RC, c = w % RC;
+    if (16 * i >= tile.nrows) break;
+    f32x4 u0 = {0.0f, 0.0f, 0.0f, 0.0f}, u1 = u0;
+    if (32 * c + 8 * g < r) {
+      const float* ur = p.u + (int64_t)p.perm[tile.row0 + min(16 * i + m, tile.nrows - 1)] * r + 32 * c + 8 * g;
+#pragma unroll 4
+      for (int s = 0; s < p.slices; ++s, ur += p.T * r) {
+        u0 += *reinterpret_cast<const f32x4*>(ur);
+        u1 += *reinterpret_cast<const f32x4*>(ur + 4);
       }
     }
-    if (bare) return;
+    const Terms<TERMS> t = split<TERMS>(u0, u1);
+#pragma unroll
+    for (int h = 0; h < TERMS; ++h) us[w * TERMS + h][lane] = t.f[h];
+  }
+  // Every wave passes one barrier: with its first chunk on the way (T4096 N16384:
+  // 79 us, 86 with the barrier first), or here without one.  Loads issued before u
+  // would delay u, which waits for its own in the order of issue (12.5 -> 16 us
+  // for 128 tokens of 64 adapters, N 16384).
+  if (n_first >= N) lds_barrier();
+  const uint16_t* const bb = p.b + (int64_t)tile.expert * p.N * r;
+  for (int n = n_first; n < N; n += n_step) {
+    uint4 y[MT][PIECES], bf[RC][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int h = 0; h < PIECES; ++h)
+        if (16 * i < tile.nrows) y[i][h] = load_y(i, h, n);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int64_t nb = min(n + col_of<BF16>(q, m), p.N - 1);
-      const uint16_t* br = p.b + ((int64_t)tile.expert * p.N + nb) * p.r + 8 * g;
+      const uint32_t at = (uint32_t)(min(n + col_of<BF16>(q, m), N - 1) * r + 8 * g);
 #pragma unroll
       for (int c = 0; c < RC; ++c) {
         bf[c][q] = make_uint4(0, 0, 0, 0);
-        if (32 * c + 8 * g < p.r) bf[c][q] = *reinterpret_cast<const uint4*>(br + 32 * c);
+        if (32 * c + 8 * g < r) bf[c][q] = *reinterpret_cast<const uint4*>(bb + at + 32 * c);
       }
     }
-  };
-  if (!bare) {
-    for (int w = wave; w < MT * RC; w += kUpWaves) {
-      const int i = w / RC, c = w % RC;
-      if (16 * i >= tile.nrows) break;
-      f32x4 u0 = {0.0f, 0.0f, 0.0f, 0.0f}, u1 = u0;
-      if (32 * c + 8 * g < p.r) {
-        const float* ur = p.u + (int64_t)p.perm[tile.row0 + min(16 * i + m, tile.nrows - 1)] * p.r + 32 * c + 8 * g;
-#pragma unroll 4
-        for (int s = 0; s < p.slices; ++s, ur += p.T * p.r) {
-          u0 += *reinterpret_cast<const f32x4*>(ur);
-          u1 += *reinterpret_cast<const f32x4*>(ur + 4);
-        }
-      }
-      const Terms<TERMS> t = split<TERMS>(u0, u1);
-#pragma unroll
-      for (int h = 0; h < TERMS; ++h) us[w * TERMS + h][lane] = t.f[h];
-    }
-  }
-  // The first chunk, on its way across the barrier.  Loaded before u it would
-  // delay u, which waits for its loads in the order of issue (12.5 -> 16 us for
-  // 128 tokens of 64 adapters, N 16384).
-  load(n_first);
-  lds_barrier();
-  for (int64_t n = n_first; n < p.N;) {
-    const int64_t nl = n + 16 / kSize * g;
+    if (n == n_first) lds_barrier();
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       if (16 * i >= tile.nrows) break;
       f32x4 acc[4] = {};
-      if (!bare) {
 #pragma unroll
-        for (int c = 0; c < RC; ++c)
+      for (int c = 0; c < RC; ++c)
 #pragma unroll
-          for (int h = TERMS - 1; h >= 0; --h) {
-            const uint4 u = us[(i * RC + c) * TERMS + h][lane];
+        for (int h = TERMS - 1; h >= 0; --h) {
+          const uint4 u = us[(i * RC + c) * TERMS + h][lane];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[q] = mfma16(bf[c][q], u, acc[q]);
-          }
-      }
+          for (int q = 0; q < 4; ++q) acc[q] = mfma16(bf[c][q], u, acc[q]);
+        }
       if (16 * i + m >= tile.nrows) continue;
 #pragma unroll
       for (int h = 0; h < PIECES; ++h) {
-        if (nl + 64 / kSize * h >= p.N) continue;
-        char* o = static_cast<char*>(p.out) + (row[i] * p.N + nl + 64 / kSize * h) * kSize;
-        uint4 v = y[i][h];
-        if constexpr (BF16) {
-          if (!bare) v = add_bf16(v, acc[2 * h], acc[2 * h + 1]);
-        } else {
-          if (!bare) v = __builtin_bit_cast(uint4, __builtin_bit_cast(f32x4, v) + acc[h]);
-        }
-        *reinterpret_cast<uint4*>(o) = v;
+        if (!inside(h, n)) continue;
+        uint4 v;
+        if constexpr (BF16)
+          v = add_bf16(y[i][h], acc[2 * h], acc[2 * h + 1]);
+        else
+          v = __builtin_bit_cast(uint4, __builtin_bit_cast(f32x4, y[i][h]) + acc[h]);
+        *reinterpret_cast<uint4*>(ob + row[i] + n * kSize + 64 * h) = v;
       }
     }
-    n += n_step;
-    if (n < p.N) load(n);
   }
+}
+
+template <bool BF16, int RC>
+__global__ __launch_bounds__(64 * kUpWaves) void lora_up_few_kernel(LoraParams p) {
+  lora_up<BF16, RC, kFewRows / 16>(p);
+}
+// Two waves per SIMD: each has 8 to 16 KiB of y on its way, and more of them only
+// scatter the accesses (T4096 N16384 on changing inputs, waves per SIMD 1, 2, 3,
+// 4: 110, 82, 83, 93 us).  The 16-token tiles want all the waves they can get
+// (128 tokens of 64 adapters with 2, 3, 8: 27, 23, 18 us).
+template <bool BF16, int RC>
+__global__ __launch_bounds__(64 * kUpWaves) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void lora_up_kernel(LoraParams p) {
+  lora_up<BF16, RC, kTileRows / 16>(p);
 }
 
 // out = y for the tokens without an adapter where the grouping does not list
@@ -613,10 +637,9 @@ hipError_t launch_lora_add(const void* y, bool bf16, int64_t T, int64_t N, const
   auto up = [&](auto rc) {
     constexpr int RC = decltype(rc)::value;
     if (l.tile_rows == kFewRows)
-      (bf16 ? lora_up_kernel<true, RC, 1> : lora_up_kernel<false, RC, 1>)<<<grid, 64 * kUpWaves, 0, s>>>(p);
+      (bf16 ? lora_up_few_kernel<true, RC> : lora_up_few_kernel<false, RC>)<<<grid, 64 * kUpWaves, 0, s>>>(p);
     else
-      (bf16 ? lora_up_kernel<true, RC, kTileRows / 16>
-            : lora_up_kernel<false, RC, kTileRows / 16>)<<<grid, 64 * kUpWaves, 0, s>>>(p);
+      (bf16 ? lora_up_kernel<true, RC> : lora_up_kernel<false, RC>)<<<grid, 64 * kUpWaves, 0, s>>>(p);
   };
   if (r32 == 1)
     up(std::integral_constant<int, 1>{});
