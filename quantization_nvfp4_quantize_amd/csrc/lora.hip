@@ -362,8 +362,8 @@ __device__ __forceinline__ Terms<TERMS> split(const f32x4& a, const f32x4& b) {
 // (token l % 16, g = l / 16) ends with columns col_of(q, 4 g + i) of its token in
 // element i of accumulator q, 16 bytes at a time, and the four g of a token with
 // 64 adjacent bytes per access; an adapter's rows of b are loaded once for the
-// tile.  Bound by y and out: 64 us of the 80 for 4096 tokens, N 16384, r 32, bf16
-// are this kernel's, 268 MB at 4.2 TB/s.  Tiles of tokens without an adapter go
+// tile.  Bound by y and out: 61 us of the 78 for 4096 tokens, N 16384, r 32, bf16
+// are this kernel's, 268 MB at 4.4 TB/s.  Tiles of tokens without an adapter go
 // the same way without a product (a loop token by token over them, 11 tiles of
 // the 75, took 70 us longer than all the others).  Workgroups of one tile are
 // launched next to each other: launched tile by tile within a chunk the same
