@@ -334,7 +334,8 @@ __global__ __launch_bounds__(1024) void lora_group_kernel(LoraParams p) {
   for (int t = tid; t < T; t += 1024) p.perm[add(place, adapter[t])] = t;
 }
 
-// Eight fp32 values -> TERMS bf16 fragments that add up to them.
+// Eight fp32 values -> TERMS bf16 fragments that add up to them; an infinite
+// value is its first term.
 template <int TERMS>
 struct Terms {
   uint4 f[TERMS];
@@ -349,7 +350,8 @@ __device__ __forceinline__ Terms<TERMS> split(const f32x4& a, const f32x4& b) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       h[i] = (__bf16)v[i];
-      v[i] -= (float)h[i];
+      const float f = (float)h[i];
+      v[i] = __builtin_fabsf(f) < INFINITY ? v[i] - f : 0.0f;  // not inf - inf
     }
     t.f[q] = __builtin_bit_cast(uint4, h);
   }

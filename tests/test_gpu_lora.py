@@ -150,6 +150,22 @@ def test_lora_rows_are_independent(nv, T):
     assert bool(torch.isnan(out[3]).all())
 
 
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("T,L", [(5, 2), (100, 2), (300, 2), (300, 40)])
+def test_lora_infinite_activation(nv, T, L, dtype):
+    """An infinite x with positive adapters gives an infinite row, as the sum
+    does, and leaves the other rows bit for bit."""
+    y, x, a, b, ids, _ = _problem(T, 256, 136, 8, L, dtype, "mixed", 11)
+    a, b = a.abs() + 2.0 ** -6, b.abs() + 2.0 ** -6
+    ids[T // 2] = L - 1
+    want = nv.lora_add(y, x, a, b, ids)
+    x[T // 2, 77] = float("inf")
+    out = nv.lora_add(y, x, a, b, ids)
+    assert torch.isposinf(out[T // 2]).all()
+    rest = torch.arange(T, device=DEV) != T // 2
+    assert torch.equal(out[rest], want[rest])
+
+
 def test_lora_repeats_bit_for_bit(nv):
     p = _problem(3000, 512, 512, 32, 9, torch.float32, "mixed", 8)
     first = nv.lora_add(*p[:5], scales=p[5])
