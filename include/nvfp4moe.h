@@ -322,8 +322,11 @@ int moe_expert_ffn_nvfp4_noalloc(const nvfp4_moe_args *args, void *stream);
  *   bias    nullable fp32 [E]
  *   logits  fp32 [T][E]
  *   Products are exact, also those of fp32 weights (whose 24 bits are used),
- *   the accumulation is fp32 in a fixed order.  x, w and logits 16-byte
- *   aligned; H and T at most 2^20 (else NVFP4_ERR_UNSUPPORTED).
+ *   the accumulation is fp32 in a fixed order.  x and w are finite: a token
+ *   with an infinite value gets logits that are not finite (with fp32 weights
+ *   also NaN where the product is infinite), the other tokens keep theirs.
+ *   x, w and logits 16-byte aligned; H and T at most 2^20 (else
+ *   NVFP4_ERR_UNSUPPORTED).
  *   Workspace: moe_router_logits_workspace_size bytes, 256-byte aligned (0:
  *   none is needed and ws may be NULL).
  */

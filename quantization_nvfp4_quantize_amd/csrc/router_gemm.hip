@@ -483,7 +483,7 @@ hipError_t launch_router_logits(const uint16_t* x, int64_t T, int H, const void*
   const GatePlan g = gate_plan(T, H, E, w_bf16);
   GateParams p{x, w, bias, g.parts > 1 ? static_cast<float*>(ws) : out, T, H, E, g.parts, g.slices};
   if (g.kind == GatePlan::kDot) {
-        auto go = [&](auto one, auto two, auto four, auto eight) {
+    auto go = [&](auto one, auto two, auto four, auto eight) {
       (T == 1 ? one : T == 2 ? two : T <= 4 ? four : eight)<<<E, kDotThreads, 0, s>>>(p);
     };
     if (w_bf16)
