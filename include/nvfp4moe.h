@@ -328,7 +328,7 @@ int moe_expert_ffn_nvfp4_noalloc(const nvfp4_moe_args *args, void *stream);
  *   x, w and logits 16-byte aligned; H and T at most 2^20 (else
  *   NVFP4_ERR_UNSUPPORTED).
  *   Workspace: moe_router_logits_workspace_size bytes, 256-byte aligned (0:
- *   none is needed and ws may be NULL).
+ *   none is needed and ws may be NULL; also for sizes that a call refuses).
  */
 size_t moe_router_logits_workspace_size(int64_t T, int64_t H, int64_t E, int w_dtype);
 int moe_router_logits(const uint16_t *x, int64_t T, int64_t H, const void *w, int w_dtype, int64_t E,

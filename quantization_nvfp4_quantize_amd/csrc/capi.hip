@@ -268,8 +268,16 @@ int nvfp4_linear(const uint16_t* x, int64_t M, int64_t K, const float* x_gs_in, 
 }
 
 // ------------------------------------------------------------------ router
+namespace {
+bool router_logits_supported(int64_t T, int64_t H, int64_t E) {
+  return H % 32 == 0 && E <= 512 && H <= ((int64_t)1 << 20) && T <= ((int64_t)1 << 20);
+}
+}  // namespace
+
 size_t moe_router_logits_workspace_size(int64_t T, int64_t H, int64_t E, int w_dtype) {
-  if (T <= 0 || H <= 0 || E <= 0) return 0;
+  // sizes that a call refuses need no workspace; the plan's products and
+  // quotients are for supported ones
+  if (T <= 0 || H <= 0 || E <= 0 || !router_logits_supported(T, H, E)) return 0;
   return nvfp4::router_logits_workspace_bytes(T, H, E, w_dtype == 0);
 }
 
@@ -279,7 +287,7 @@ int moe_router_logits(const uint16_t* x, int64_t T, int64_t H, const void* w, in
   if (T < 0 || H < 1 || E < 1) return fail(NVFP4_ERR_INVALID_ARG, "moe_router_logits: need T >= 0, H >= 1, E >= 1");
   if (w_dtype != 0 && w_dtype != 1)
     return fail(NVFP4_ERR_INVALID_ARG, "moe_router_logits: w_dtype must be 0 (bf16) or 1 (fp32)");
-  if (H % 32 != 0 || E > 512 || H > ((int64_t)1 << 20) || T > ((int64_t)1 << 20))
+  if (!router_logits_supported(T, H, E))
     return fail(NVFP4_ERR_UNSUPPORTED,
                 "moe_router_logits: need H %% 32 == 0, H <= 2^20, E <= 512 and T <= 2^20 (T=%lld H=%lld E=%lld)",
                 (long long)T, (long long)H, (long long)E);

@@ -72,3 +72,13 @@ def test_router_logits_workspace_and_empty(nv):
 def test_router_logits_binding_rejects_host_tensors(nv):
     with pytest.raises(ValueError, match="GPU"):
         nv.router_logits(torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(8, 64, dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("T,H,E", [(1 << 62, 64, 1 << 62), (1 << 40, 1 << 40, 1 << 40), ((1 << 63) - 1, 64, 8),
+                                   (9, 1 << 62, 4), ((1 << 20) + 1, 64, 8), (16, (1 << 20) + 32, 8), (16, 64, 513),
+                                   (4096, 48, 8)])
+@pytest.mark.parametrize("w_dtype", [0, 1])
+def test_router_logits_workspace_of_unsupported_sizes(nv, T, H, E, w_dtype):
+    """A size query answers for sizes that a call refuses as well (0: no workspace)."""
+    assert nv._lib.moe_router_logits_workspace_size(T, H, E, w_dtype) == 0
+    assert _logits(nv, T=T, H=H, E=E, w_dtype=w_dtype) == -2
