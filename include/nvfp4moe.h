@@ -155,6 +155,8 @@ int nvfp4_linear(const uint16_t *x, int64_t M, int64_t K, const float *x_gs_in, 
  *   ids     int32 [T], scales nullable fp32 [L] (1 without)
  *   out     [T][N], the type of y; y itself (in place) or a buffer that does
  *           not overlap it.  In place, rows without an adapter are not touched.
+ *           out may lie over x (read before out is written); out and ws over
+ *           anything else that the call reads are refused.
  *   Products are exact and accumulated in fp32; a[id] x[t] goes into the
  *   second product with 16 bits (bf16 output) or 24 (fp32); one rounding of
  *   the sum to the output's type.  A token's result does not depend on the

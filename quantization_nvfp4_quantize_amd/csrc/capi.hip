@@ -33,6 +33,18 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
+// Memory of one operand, and whether two share a byte (an absent one has none).
+struct Span {
+  const void* p;
+  size_t bytes;
+  const char* name;
+};
+
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+}
+
 }  // namespace
 
 extern "C" {
@@ -376,6 +388,19 @@ int nvfp4_lora_add(const void* y, int dtype, int64_t T, int64_t N, const uint16_
   if (!ws || ws_bytes < need)
     return fail(NVFP4_ERR_WORKSPACE, "nvfp4_lora_add: workspace %zu < %zu bytes", ws_bytes, need);
   if (!aligned(ws, 256)) return fail(NVFP4_ERR_INVALID_ARG, "nvfp4_lora_add: ws must be 256-byte aligned");
+  // Everything that is read while out or the workspace is written.  x is read
+  // by the first product only, which ends before out is written.
+  const size_t ab = (size_t)L * (size_t)r * sizeof(uint16_t);
+  const Span o{out, bytes, "out"}, w{ws, need, "ws"}, xs{x, (size_t)T * (size_t)K * sizeof(uint16_t), "x"},
+      ys{y, bytes, "y"};
+  const Span in[] = {{a, ab * (size_t)K, "a"},
+                     {b, ab * (size_t)N, "b"},
+                     {ids, (size_t)T * sizeof(int32_t), "ids"},
+                     {scales, (size_t)L * sizeof(float), "scales"}};
+  for (const Span& i : in)
+    if (overlap(o, i)) return fail(NVFP4_ERR_INVALID_ARG, "nvfp4_lora_add: out and %s overlap", i.name);
+  for (const Span& i : {o, xs, ys, in[0], in[1], in[2], in[3]})
+    if (overlap(w, i)) return fail(NVFP4_ERR_INVALID_ARG, "nvfp4_lora_add: ws and %s overlap", i.name);
   return hip_status(nvfp4::launch_lora_add(y, dtype == 0, T, N, x, (int)K, a, b, (int)r, (int)L, ids, scales, out, ws,
                                            reinterpret_cast<hipStream_t>(stream)),
                     "nvfp4_lora_add");

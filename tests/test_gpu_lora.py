@@ -279,3 +279,21 @@ def test_lora_beside_the_projection_the_router_and_the_experts(nv):
         torch.cuda.synchronize()
         for p, q in zip(held, now):
             assert torch.equal(p, q), i
+
+
+@pytest.mark.parametrize("T", [9, 700, 17000])
+def test_lora_output_over_its_input(nv, T):
+    """out may be x's memory, also where that is y's; out over b is refused."""
+    p = _problem(T, 128, 128, 16, 5, BF, "mixed", 6)
+    want = nv.lora_add(*p[:5], scales=p[5])
+    x = p[1].clone()
+    assert torch.equal(nv.lora_add(p[0], x, *p[2:5], scales=p[5], out=x), want)
+    want = nv.lora_add(p[1], *p[1:5], scales=p[5])
+    x = p[1].clone()
+    assert torch.equal(nv.lora_add(x, x, *p[2:5], scales=p[5], out=x), want)
+    L, N, r = p[3].shape
+    room = torch.zeros(L * N * r + T * N, dtype=BF, device=DEV)
+    room[:L * N * r] = p[3].flatten()
+    b, over = room[:L * N * r].view(L, N, r), room[L * N * r - 8 * N:][:T * N].view(T, N)
+    with pytest.raises(nv.Nvfp4Error, match="out and b overlap"):
+        nv.lora_add(*p[:3], b, p[4], scales=p[5], out=over)

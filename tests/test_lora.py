@@ -58,3 +58,32 @@ def test_lora_binding_rejects_host_tensors(nv):
     with pytest.raises(ValueError, match="GPU"):
         nv.lora_add(torch.zeros(4, 64, dtype=h), torch.zeros(4, 32, dtype=h), torch.zeros(2, 8, 32, dtype=h),
                     torch.zeros(2, 64, 8, dtype=h), torch.zeros(4, dtype=torch.int32))
+
+
+def _apart(nv, T=4, N=64, K=64, r=8, L=2, **over):
+    """Operands 1 MiB apart (16 KiB and less each), some of them moved."""
+    at = {n: (i + 1) << 20 for i, n in enumerate(("y", "x", "a", "b", "ids", "scales", "out", "ws"))}
+    at.update(over)
+    need = nv._lib.nvfp4_lora_add_workspace_size(T, N, K, r, L)
+    p = {n: ctypes.c_void_p(v) for n, v in at.items()}
+    return nv._lib.nvfp4_lora_add(p["y"], 0, T, N, p["x"], K, p["a"], p["b"], r, L, p["ids"], p["scales"], p["out"],
+                                  p["ws"], need, None)
+
+
+# bytes of a, b, ids, scales for T 4, N 64, K 64, r 8, L 2; out has 512
+@pytest.mark.parametrize("name,at,size", [("a", 3 << 20, 2048), ("b", 4 << 20, 2048), ("ids", 5 << 20, 16),
+                                          ("scales", 6 << 20, 8)])
+def test_lora_refuses_an_output_over_what_it_reads(nv, name, at, size):
+    for out in (at, at - 512 + 16, at + (size - 1) // 16 * 16):
+        assert _apart(nv, out=out) == -1
+        assert b"out and %s overlap" % name.encode() in nv._lib.nvfp4_last_error()
+
+
+@pytest.mark.parametrize("name,at,size", [("y", 1 << 20, 512), ("x", 2 << 20, 512), ("a", 3 << 20, 2048),
+                                          ("b", 4 << 20, 2048), ("ids", 5 << 20, 16), ("scales", 6 << 20, 8),
+                                          ("out", 7 << 20, 512)])
+def test_lora_refuses_a_workspace_over_its_operands(nv, name, at, size):
+    need = nv._lib.nvfp4_lora_add_workspace_size(4, 64, 64, 8, 2)
+    for ws in (at, at - (need - 1) // 256 * 256, at + (size - 1) // 256 * 256):
+        assert _apart(nv, ws=ws) == -1
+        assert b"ws and %s overlap" % name.encode() in nv._lib.nvfp4_last_error()
