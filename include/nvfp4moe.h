@@ -322,7 +322,8 @@ int moe_expert_ffn_nvfp4_noalloc(const nvfp4_moe_args *args, void *stream);
  *   x       bf16 [T][H], H % 32 == 0
  *   w       [E][H], bf16 (w_dtype 0) or fp32 (1); 1 <= E <= 512
  *   bias    nullable fp32 [E]
- *   logits  fp32 [T][E]
+ *   logits  fp32 [T][E]; like the workspace over none of the other operands
+ *           (else NVFP4_ERR_INVALID_ARG)
  *   Products are exact, also those of fp32 weights (whose 24 bits are used),
  *   the accumulation is fp32 in a fixed order.  x and w are finite: a token
  *   with an infinite value gets logits that are not finite (with fp32 weights

@@ -311,6 +311,16 @@ int moe_router_logits(const uint16_t* x, int64_t T, int64_t H, const void* w, in
   if (need && (!ws || ws_bytes < need))
     return fail(NVFP4_ERR_WORKSPACE, "moe_router_logits: workspace %zu < %zu bytes", ws_bytes, need);
   if (need && !aligned(ws, 256)) return fail(NVFP4_ERR_INVALID_ARG, "moe_router_logits: ws must be 256-byte aligned");
+  // x, w and bias are read while logits and the workspace are written
+  const size_t row = (size_t)H * sizeof(uint16_t);
+  const Span o{logits, (size_t)T * (size_t)E * sizeof(float), "logits"}, wk{need ? ws : nullptr, need, "ws"};
+  const Span in[] = {{x, (size_t)T * row, "x"},
+                     {w, (size_t)E * row * (w_dtype == 0 ? 1 : 2), "w"},
+                     {bias, (size_t)E * sizeof(float), "bias"}};
+  for (const Span& i : in)
+    if (overlap(o, i)) return fail(NVFP4_ERR_INVALID_ARG, "moe_router_logits: logits and %s overlap", i.name);
+  for (const Span& i : {o, in[0], in[1], in[2]})
+    if (overlap(wk, i)) return fail(NVFP4_ERR_INVALID_ARG, "moe_router_logits: ws and %s overlap", i.name);
   return hip_status(nvfp4::launch_router_logits(x, T, (int)H, w, w_dtype == 0, (int)E, bias, logits, ws,
                                                 reinterpret_cast<hipStream_t>(stream)),
                     "moe_router_logits");

@@ -82,3 +82,32 @@ def test_router_logits_workspace_of_unsupported_sizes(nv, T, H, E, w_dtype):
     """A size query answers for sizes that a call refuses as well (0: no workspace)."""
     assert nv._lib.moe_router_logits_workspace_size(T, H, E, w_dtype) == 0
     assert _logits(nv, T=T, H=H, E=E, w_dtype=w_dtype) == -2
+
+
+def _logits_apart(nv, T, w_dtype, H=64, E=8, **over):
+    """Operands 4 MiB apart, some of them moved; returns the status."""
+    at = {n: (i + 1) << 22 for i, n in enumerate(("x", "w", "bias", "out", "ws"))}
+    at.update(over)
+    p = {n: ctypes.c_void_p(v) for n, v in at.items()}
+    return _logits(nv, p["x"], T, H, p["w"], w_dtype, E, p["bias"], p["out"], p["ws"],
+                   nv._lib.moe_router_logits_workspace_size(T, H, E, w_dtype))
+
+
+@pytest.mark.parametrize("T", [4, 40, 8200])
+@pytest.mark.parametrize("w_dtype", [0, 1])
+def test_router_logits_refuses_an_output_over_its_inputs(nv, T, w_dtype):
+    for name, at, size in (("x", 1 << 22, T * 128), ("w", 2 << 22, 8 * 128 * (1 + w_dtype)), ("bias", 3 << 22, 32)):
+        for out in (at, at - T * 32 + 16, at + (size - 1) // 16 * 16):
+            assert _logits_apart(nv, T, w_dtype, out=out) == -1
+            assert b"logits and %s overlap" % name.encode() in nv._lib.nvfp4_last_error()
+
+
+def test_router_logits_refuses_a_workspace_over_its_operands(nv):
+    T, H, E = 40, 7168, 8                     # slices of K: partial sums in the workspace
+    need = nv._lib.moe_router_logits_workspace_size(T, H, E, 0)
+    assert need > 0
+    for name, at, size in (("x", 1 << 22, T * H * 2), ("w", 2 << 22, E * H * 2), ("bias", 3 << 22, 32),
+                           ("logits", 4 << 22, T * E * 4)):
+        for ws in (at, at - (need - 1) // 256 * 256, at + (size - 1) // 256 * 256):
+            assert _logits_apart(nv, T, 0, H=H, ws=ws) == -1
+            assert b"ws and %s overlap" % name.encode() in nv._lib.nvfp4_last_error()
