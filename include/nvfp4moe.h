@@ -365,8 +365,8 @@ int moe_router_logits(const uint16_t *x, int64_t T, int64_t H, const void *w, in
  * Requirements: T >= 0, 1 <= E <= 512, 1 <= k <= 32 (else
  * NVFP4_ERR_UNSUPPORTED), n_group divides E and is at most 64,
  * 1 <= topk_group <= n_group, k <= topk_group * (E / n_group), T <= 2^24;
- * logits aligned to 16 bytes.  No workspace; ids and weights must not overlap
- * the logits.
+ * logits aligned to 16 bytes.  No workspace; ids and weights over each other
+ * or over logits, bias or n_tokens are refused (NVFP4_ERR_INVALID_ARG).
  */
 int moe_route(const void *logits, int logits_dtype, int64_t T, int64_t E, int64_t k, int scoring, const float *bias,
               int64_t n_group, int64_t topk_group, int group_top, int renormalize, float scale,

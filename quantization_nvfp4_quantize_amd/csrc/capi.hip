@@ -351,6 +351,16 @@ int moe_route(const void* logits, int logits_dtype, int64_t T, int64_t E, int64_
   if (!logits || !ids || !weights) return fail(NVFP4_ERR_INVALID_ARG, "moe_route: null pointer");
   if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(n_tokens, 4) || !aligned(ids, 4) || !aligned(weights, 4))
     return fail(NVFP4_ERR_INVALID_ARG, "moe_route: misaligned pointer (logits need 16 bytes)");
+  // other waves still read while a wave writes its token
+  const size_t picks = (size_t)T * (size_t)k * 4;
+  const Span o{ids, picks, "ids"}, wt{weights, picks, "weights"};
+  const Span in[] = {{logits, (size_t)T * (size_t)E * (logits_dtype == 0 ? 2 : 4), "logits"},
+                     {bias, (size_t)E * sizeof(float), "bias"},
+                     {n_tokens, sizeof(int32_t), "n_tokens"}};
+  if (overlap(o, wt)) return fail(NVFP4_ERR_INVALID_ARG, "moe_route: ids and weights overlap");
+  for (const Span& i : in)
+    for (const Span& w : {o, wt})
+      if (overlap(w, i)) return fail(NVFP4_ERR_INVALID_ARG, "moe_route: %s and %s overlap", w.name, i.name);
   return hip_status(nvfp4::launch_moe_route(logits, logits_dtype == 0, T, (int)E, bias, scoring == 1, (int)k,
                                             (int)n_group, (int)topk_group, group_top, renormalize == 1, scale,
                                             n_tokens, ids, weights, reinterpret_cast<hipStream_t>(stream)),

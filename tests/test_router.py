@@ -111,3 +111,17 @@ def test_router_logits_refuses_a_workspace_over_its_operands(nv):
         for ws in (at, at - (need - 1) // 256 * 256, at + (size - 1) // 256 * 256):
             assert _logits_apart(nv, T, 0, H=H, ws=ws) == -1
             assert b"ws and %s overlap" % name.encode() in nv._lib.nvfp4_last_error()
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_route_refuses_outputs_over_its_operands(nv, dtype):
+    T, E, k = 40, 64, 8
+    at = {n: (i + 1) << 20 for i, n in enumerate(("logits", "bias", "n_tokens", "ids", "w"))}
+    size = {"logits": T * E * (2 + 2 * dtype), "bias": 4 * E, "n_tokens": 4, "ids": 4 * T * k, "w": 4 * T * k}
+    for out, name in (("ids", b"ids"), ("w", b"weights")):
+        for over in set(at) - {out}:
+            for p in (at[over], at[over] - size[out] + 4, at[over] + size[over] - 4):
+                now = {n: ctypes.c_void_p(v) for n, v in {**at, out: p}.items()}
+                assert _route(nv, T=T, E=E, k=k, dtype=dtype, **now) == -1
+                error = nv._lib.nvfp4_last_error()
+                assert b"overlap" in error and name in error
