@@ -128,6 +128,16 @@ def _workspace(nbytes, device):
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+def _ws_bytes(ws, device):
+    """Size of a caller's workspace; its elements have to be memory of their own
+    (an expanded view counts bytes that are not there)."""
+    if ws.device != device:
+        raise ValueError(f"ws must be on {device}, got {ws.device}")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.numel() * ws.element_size()
+
+
 def _require_all(device, *specs):
     """Each (tensor or None, dtype, shape, name) on the device and contiguous:
     _require in one pass over the tensors of a short call."""
@@ -270,14 +280,13 @@ def lora_add(y, x, a, b, ids, scales=None, out=None, ws=None):
     _require_all(dev, (y, y.dtype, (T, N), "y"), (x, torch.bfloat16, (T, K), "x"),
                  (a, torch.bfloat16, (L, r, K), "a"), (b, torch.bfloat16, (L, N, r), "b"),
                  (ids, torch.int32, (T,), "ids"), (scales, torch.float32, (L,), "scales"), (out, y.dtype, (T, N), "out"))
-    if ws is not None and ws.device != dev:
-        raise ValueError(f"ws must be on {dev}")
     if out is None:
         out = torch.empty_like(y)
     if ws is None:
         ws = _workspace(_lib.nvfp4_lora_add_workspace_size(T, N, K, r, L), dev)
+    nws = _ws_bytes(ws, dev)
     _launch("nvfp4_lora_add", dev, _at(y), 0 if y.dtype == torch.bfloat16 else 1, T, N, _at(x), K, _at(a), _at(b), r,
-            L, _at(ids), _at(scales), _at(out), _at(ws), ws.numel())
+            L, _at(ids), _at(scales), _at(out), _at(ws), nws)
     return out
 
 
@@ -350,16 +359,14 @@ def router_logits(x, w, bias=None, out=None, ws=None):
     (T, H), E, dev = x.shape, w.shape[0], x.device
     _require_all(dev, (x, torch.bfloat16, (T, H), "x"), (w, w.dtype, (E, H), "w"), (bias, torch.float32, (E,), "bias"),
                  (out, torch.float32, (T, E), "out"))
-    if ws is not None and ws.device != dev:
-        raise ValueError(f"ws must be on {dev}")
     if out is None:
         out = torch.empty((T, E), dtype=torch.float32, device=dev)
     code = 0 if w.dtype == torch.bfloat16 else 1
     if ws is None:
         need = _lib.moe_router_logits_workspace_size(T, H, E, code)
         ws = _workspace(need, dev) if need else None
-    _launch("moe_router_logits", dev, _at(x), T, H, _at(w), code, E, _at(bias), _at(out), _at(ws),
-            0 if ws is None else ws.numel())
+    nws = 0 if ws is None else _ws_bytes(ws, dev)
+    _launch("moe_router_logits", dev, _at(x), T, H, _at(w), code, E, _at(bias), _at(out), _at(ws), nws)
     return out
 
 

@@ -297,3 +297,22 @@ def test_lora_output_over_its_input(nv, T):
     b, over = room[:L * N * r].view(L, N, r), room[L * N * r - 8 * N:][:T * N].view(T, N)
     with pytest.raises(nv.Nvfp4Error, match="out and b overlap"):
         nv.lora_add(*p[:3], b, p[4], scales=p[5], out=over)
+
+
+def test_workspaces_are_memory_of_their_own(nv):
+    """A workspace counts in bytes, whatever its type; an expanded view, whose
+    elements share memory, a short one and one on the host are refused."""
+    p = _problem(40, 7168, 64, 16, 3, BF, "one", 0)
+    gate = torch.randn(8, 7168, device=DEV).to(BF)
+    for call, need in ((lambda ws: nv.lora_add(*p[:5], ws=ws), nv.lora_add_workspace(40, 64, 7168, 16, 3, DEV).numel()),
+                       (lambda ws: nv.router_logits(p[1], gate, ws=ws),
+                        nv._lib.moe_router_logits_workspace_size(40, 7168, 8, 0))):
+        assert need > 256
+        want = call(None)
+        assert torch.equal(call(torch.empty(need // 4, device=DEV)), want)
+        with pytest.raises(ValueError, match="contiguous"):
+            call(torch.empty(1, dtype=torch.uint8, device=DEV).expand(need))
+        with pytest.raises(ValueError, match="ws must be on"):
+            call(torch.empty(need, dtype=torch.uint8))
+        with pytest.raises(nv.Nvfp4Error, match="workspace"):
+            call(torch.empty(need - 1, dtype=torch.uint8, device=DEV))
