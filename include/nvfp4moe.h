@@ -159,7 +159,9 @@ int nvfp4_linear(const uint16_t *x, int64_t M, int64_t K, const float *x_gs_in, 
  *           anything else that the call reads are refused.
  *   Products are exact and accumulated in fp32; a[id] x[t] goes into the
  *   second product with 16 bits (bf16 output) or 24 (fp32); one rounding of
- *   the sum to the output's type.  A token's result does not depend on the
+ *   the sum to the output's type.  x, a and b are finite: an infinite x or a
+ *   goes through the sums as such, an infinite b makes its column's results
+ *   infinite or NaN; tokens without such a value keep theirs.  A token's result does not depend on the
  *   other tokens of the call beyond the fp32 summation order of a[id] x[t].
  *   T >= 0; K % 32 == 0, N % 8 == 0, r % 8 == 0, r <= 128, L <= 512 and T, K,
  *   N <= 2^20 (else NVFP4_ERR_UNSUPPORTED).  y, x, a, b, out

@@ -335,7 +335,8 @@ __global__ __launch_bounds__(1024) void lora_group_kernel(LoraParams p) {
 }
 
 // Eight fp32 values -> TERMS bf16 fragments that add up to them; an infinite
-// value is its first term.
+// value is its first term.  A finite value beyond the largest bf16 (it would
+// round to infinity) leaves the excess to the next term.
 template <int TERMS>
 struct Terms {
   uint4 f[TERMS];
@@ -349,7 +350,8 @@ __device__ __forceinline__ Terms<TERMS> split(const f32x4& a, const f32x4& b) {
     bf16x8 h;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      h[i] = (__bf16)v[i];
+      const float most = 0x1.fep127f, w = __builtin_fabsf(v[i]);
+      h[i] = (__bf16)(w > most && w < INFINITY ? __builtin_copysignf(most, v[i]) : v[i]);
       const float f = (float)h[i];
       v[i] = __builtin_fabsf(f) < INFINITY ? v[i] - f : 0.0f;  // not inf - inf
     }

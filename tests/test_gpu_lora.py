@@ -316,3 +316,22 @@ def test_workspaces_are_memory_of_their_own(nv):
             call(torch.empty(need, dtype=torch.uint8))
         with pytest.raises(nv.Nvfp4Error, match="workspace"):
             call(torch.empty(need - 1, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("T,L", [(5, 2), (100, 2), (300, 2), (300, 40)])
+def test_lora_inner_result_next_to_the_largest_value(nv, T, L, dtype):
+    """a x beyond the largest bf16 and still finite: the outputs are finite too."""
+    y, x, a, b, ids, _ = _problem(T, 256, 136, 8, L, dtype, "mixed", 13)
+    most = torch.finfo(BF).max
+    x.zero_()
+    x[:, 5], x[:, 200] = most, most / 256  # 1.0039 times the largest bf16: rounds to infinity
+    a.zero_()
+    a[:, ::2, 5], a[:, ::2, 200] = 1.0, 1.0
+    a[:, 1::2, 5], a[:, 1::2, 200] = -1.0, -1.0
+    b.mul_(2.0 ** -110)
+    b[:, ::3] = 0.0
+    ids[T // 2] = L - 1
+    out = nv.lora_add(y, x, a, b, ids)
+    assert bool(torch.isfinite(out).all())
+    _check(out, y, x, a, b, ids, None)
