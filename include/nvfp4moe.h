@@ -355,9 +355,13 @@ int moe_router_logits(const uint16_t *x, int64_t T, int64_t H, const void *w, in
  *           group's value is the sum of its group_top (1 or 2) largest
  *           choice values (score, plus bias).  1, 1, 1: no groups.
  *   ids     int32 [T][k]: the k best choices of the groups in use, best
- *           first.  The order is that of the exact values (where fp32 could
- *           not tell two apart, fp64 decides); ties go to the lowest index,
- *           for experts and for groups.  With fewer than k experts to choose
+ *           first.  Without a bias the logits order the experts (and groups
+ *           with group_top 1); else choice and group values do, as fp64 holds
+ *           them (fp32 decides only where its errors cannot matter).  Values
+ *           that are one in fp64 tie: sigmoids of logits beyond 37, softmax
+ *           scores that underflow, scores that a bias swallows.  Ties go to
+ *           the lowest index, for experts and for groups.  With fewer than k
+ *           experts to choose
  *           from the remaining ids are -1, which moe_expert_ffn_nvfp4 skips.
  *   weights fp32 [T][k]: scale * score, or with renormalize 1 scale * score /
  *           (sum of the token's chosen scores); 0 where the id is -1

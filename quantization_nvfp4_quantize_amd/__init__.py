@@ -377,6 +377,8 @@ def route(logits, topk, scoring="softmax", bias=None, n_group=1, topk_group=1, g
           scale=1.0, n_tokens=None, out=None):
     """Routing of tokens to experts: logits [T][E] (bf16 or float32) -> (ids
     int32 [T][topk], weights float32 [T][topk]), as moe_expert_ffn takes them.
+    The logits start at a multiple of 16 bytes (a slice of rows with an odd E
+    may need a copy).
 
     scoring: "softmax" (over the token's experts) or "sigmoid".  bias: float32
     [E], added to the scores for the choice only.  n_group, topk_group,

@@ -10,11 +10,12 @@
 //           its group_top (1 or 2) largest choices; the topk_group best stay
 //   ids     the k largest choices of the groups that stay, descending
 //   weight  scale * s_e, or scale * s_e / (sum of the k chosen scores)
-// Ties go to the lowest index.  The order is that of the exact values: scores
-// in fp32 carry errors of a few 2^-24, so a decision between two values
-// closer than a bound on those errors (below) is taken again in fp64, for the
-// whole token.  Choices spread over a few hundredths put fewer than 1 % of the
-// tokens there.
+// Ties go to the lowest index.  The order is that of the values above in fp64,
+// where those that fp64 cannot separate (sigmoids of logits beyond 37, softmax
+// terms that underflow, scores that a bias swallows) tie.  Scores in fp32 carry
+// errors of up to some 30 * 2^-24, so a decision between two values closer than
+// a bound on those errors (at kGap) is taken again in fp64, for the whole
+// token.
 //
 // One wave holds one token; lane l the v experts g S + (l % Lg) v + 0 .. v-1
 // of group g = l / Lg, with Lg = 64 / (n_group rounded up to a power of two)
@@ -156,6 +157,20 @@ __device__ __forceinline__ float first_lanes(float x, int k, Op op) {
   for (int s = 0; s < 4; ++s) x = op(x, swap_step(x, s));
   return k > 16 ? op(x, swap_step(x, 4)) : x;
 }
+
+// The gap up to which two choices c = s + bias may be in the wrong order in fp32,
+// in units of u = 2^-24, the largest relative error of one rounding.
+// Softmax, x = z - mx: a numerator exp(x) is off by (2.25 |x| + 2) u (difference,
+// product with a rounded constant, exp2); the sum by that of its terms in the
+// mean plus 20 u (14 additions of a lane's at most 15 experts, 6 of the lanes),
+// its reciprocal by 2 u, the product by u.  Sum and reciprocal move all scores of
+// a token by one factor, so the difference of two is off by
+//   |s1 - s2| (24 + 2.25 sum_e s_e |x_e|) u + s1 (2.25 |x1| + 3) u + s2 (2.25 |x2| + 3) u,
+// at most 27.1 u over all scores that add up to 1, and below 32 u for the sums of
+// two scores of two groups.  Sigmoid: s (1 - s) (2.25 |z| + 2) u + 3 u < 5 u per
+// score.  Then |c| u for each choice's own rounding: 32 u + 4 |c| u covers two
+// choices, twice that two sums of two, which are rounded themselves.
+constexpr float kGap = 0x1p-19f, kGapBias = 0x1p-22f;
 
 // Scores of a lane's experts (0 for masked ones); mx, sum: the softmax's
 // maximum and sum over the token (all lanes).
@@ -356,10 +371,9 @@ __global__ __launch_bounds__(64 * kRouteRows) void moe_route_kernel(RouteParams 
       const bool keep = keep_group(p, value, group);
       if (by_score) {
         // the worst group that stays against the best that goes: two sums of
-        // two choices c, each off by at most 2^-20 + 2^-24 |c|, and rounded;
-        // equal or infinite values count as close.  Scores are at most 1; with
-        // a bias the largest |c| bounds the errors (a sum may be small where
-        // its terms are not).
+        // two choices; equal or infinite values count as close.  Scores are at
+        // most 1; with a bias the largest |c| bounds the errors (a sum may be
+        // small where its terms are not).
         const bool in = group < p.n_group;
         const uint32_t kv = key_of(value);
         const uint32_t low = ~wave_max(in && keep ? ~kv : 0u), high = wave_max(in && !keep ? kv : 0u);
@@ -370,7 +384,7 @@ __global__ __launch_bounds__(64 * kRouteRows) void moe_route_kernel(RouteParams 
           for (int j = 0; j < V; ++j) m = max(m, key[j] ? __float_as_uint(value_of(key[j])) & 0x7fffffffu : 0u);
           most = __uint_as_float(wave_max(m));
         }
-        unsure = high != 0u && !(value_of(low) - value_of(high) > 0x1p-18f + 0x1p-21f * most);
+        unsure = high != 0u && !(value_of(low) - value_of(high) > 2.0f * kGap + 2.0f * kGapBias * most);
       }
       if (!keep) {
 #pragma unroll
@@ -416,12 +430,10 @@ __global__ __launch_bounds__(64 * kRouteRows) void moe_route_kernel(RouteParams 
       }
     }
     if (p.bias) {
-      // every pick against the next: a choice is off by at most 2^-20 (the score's
-      // exponentials and sum) + 2^-24 |c| (its own rounding), two of them by twice
-      // that; a NaN gap (inf - inf) counts as close
+      // every pick against the next; a NaN gap (inf - inf) counts as close
       const uint32_t next_key = (uint32_t)__shfl_down((int)my_key, 1);
       const float c = value_of(my_key), next = value_of(next_key);
-      unsure = unsure || __ballot(lane + 1 < n_picked && !(c - next > 0x1p-19f + 0x1p-22f * fabsf(next))) != 0;
+      unsure = unsure || __ballot(lane + 1 < n_picked && !(c - next > kGap + kGapBias * fabsf(next))) != 0;
     }
     if (lane >= p.k) my_e = -1;
   }

@@ -253,6 +253,42 @@ def test_route_feeds_the_expert_ffn(nv):
     assert float((y - y2).norm() / y2.norm()) <= 64 * 2.0 ** -24
 
 
+def test_route_orders_by_what_64_bits_hold(nv):
+    """With a bias, scores that are one value in 64 bits tie and go by index;
+    one step before that the larger logit is first; without a bias the logits
+    decide throughout."""
+    bias = torch.zeros(4, device=DEV)
+    for scoring, apart, same in (("sigmoid", [34.0, 34.5, 33.0, -1.0], [40.0, 41.0, 60.0, -1.0]),
+                                 ("softmax", [-700.0, -699.0, -701.0, 0.0], [-800.0, -799.0, -801.0, 0.0])):
+        z = torch.tensor([apart, same], device=DEV)
+        ids, _ = _check(nv, z, 4, bias=bias, scoring=scoring)
+        first = 1 if scoring == "softmax" else 0
+        assert host(ids)[:, first:first + 3].tolist() == [[1, 0, 2], [0, 1, 2]]
+        ids, _ = _check(nv, z, 4, scoring=scoring)
+        assert host(ids)[:, first:first + 3].tolist() == [[1, 0, 2], [2, 1, 0] if scoring == "sigmoid" else [1, 0, 2]]
+    # group sums without a bias: 1 + 1 in both, then in the logits' order inside the group that stays
+    z = torch.tensor([[40.0, 41.0, 50.0, 51.0], [33.0, 34.0, 50.0, 51.0]], device=DEV)
+    ids, _ = _check(nv, z, 2, scoring="sigmoid", n_group=2, topk_group=1, group_top=2)
+    assert host(ids).tolist() == [[1, 0], [3, 2]]
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,n_group", [(256, 1), (512, 1), (510, 3), (510, 5), (504, 9), (510, 17), (495, 33)])
+@pytest.mark.parametrize("std", [0.02, 2.0])
+def test_route_small_gaps_with_every_lane_layout(nv, scoring, E, n_group, std):
+    """One to fifteen experts per lane, flat and peaked scores, biases that
+    bring the choices of neighbours to within a few roundings of fp32."""
+    z = _logits(24, E, E + n_group, std=std)
+    z[:, 3] += 4.0                   # with a score next to 1 the sum's error weighs most
+    s = torch.softmax(z.double(), 1) if scoring == "softmax" else torch.sigmoid(z.double())
+    g = torch.Generator().manual_seed(E)
+    step = torch.randint(-40, 41, (E,), generator=g).to(DEV).double() * 2.0 ** -25
+    for t in range(0, 24, 3):
+        bias = (0.5 - s[t] + step).float()
+        _check(nv, z[t:t + 1].clone(), 8, bias=bias, scoring=scoring, n_group=n_group, topk_group=max(1, n_group // 2),
+               group_top=2 if n_group > 1 else 1)
+
+
 # ------------------------------------------------------------------ gate projection
 def _gate(T, H, E, dtype, seed):
     g = torch.Generator().manual_seed(seed)
