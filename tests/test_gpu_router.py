@@ -398,3 +398,77 @@ def test_router_logits_refuses_bad_tensors(nv):
     with pytest.raises(nv.Nvfp4Error):
         nv.router_logits(x[:, :48].contiguous(), w[:, :48].contiguous())
     assert nv.router_logits(x[:0], w).shape == (0, 8)
+
+
+# Sizes beyond the sliced kernel's range for both weight types, which the tiled
+# kernel takes: one K step and odd numbers of them, a last tile of few tokens,
+# one part (the bias and the store in the kernel itself) and several, whole and
+# cut register quads of experts, more experts than one tile, few of them; the
+# first sizes on either side of the border between the kernels
+TILE_SHAPES = [(16387, 512, 256), (16500, 448, 255), (40000, 64, 300), (70001, 576, 4), (4100, 1024, 256),
+               (1100, 7168, 128), (2100, 4096, 101), (3000, 2048, 512), (8191, 320, 260), (2048, 1024, 256),
+               (2049, 1024, 256), (2816, 1024, 256), (2817, 1024, 256)]
+
+
+@pytest.mark.parametrize("T,H,E", TILE_SHAPES)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_router_logits_tiles(nv, T, H, E, dtype):
+    x, w, b = _gate(T, H, E, dtype, T + H + E)
+    _gate_check(nv.router_logits(x, w), x, w, None)
+    room = torch.full((T * E + 8,), 9.0, device=DEV)
+    y = nv.router_logits(x, w, bias=b, out=room[:T * E].view(T, E))
+    _gate_check(y, x, w, b)
+    assert bool((room[T * E:] == 9.0).all())
+
+
+@pytest.mark.parametrize("T,H,E", [(5000, 2048, 160), (5001, 2048, 159), (20000, 512, 130)])
+def test_router_logits_tiles_use_all_bits_of_a_32_bit_weight(nv, T, H, E):
+    w = torch.zeros(E, H, device=DEV)
+    g = torch.Generator().manual_seed(1)
+    v = (torch.rand(E, generator=g) + 1.0).to(DEV)
+    nxt = torch.nextafter(v, torch.full_like(v, 2.0))
+    e = torch.arange(E, device=DEV)
+    w[e, 3 * e], w[e, 3 * e + 1] = v, nxt
+    x = torch.zeros(T, H, device=DEV)
+    x[:, 0::3], x[:, 1::3] = -1.0, 1.0  # of an expert's two weights, whatever else lies there is zero
+    y = nv.router_logits(x.bfloat16(), w)
+    assert torch.equal(y, (nxt - v).expand(T, E))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H,E", [(4500, 2048, 160), (16500, 512, 96)])
+def test_router_logits_tile_rows_are_independent(nv, T, H, E, dtype):
+    x, w, _ = _gate(T, H, E, dtype, 3)
+    y0 = nv.router_logits(x, w)
+    x2 = x.clone()
+    x2[1], x2[T - 1, 7], x2[130, H - 1] = NAN, INF, -INF
+    y = nv.router_logits(x2, w)
+    keep = torch.ones(T, dtype=torch.bool, device=DEV)
+    keep[[1, 130, T - 1]] = False
+    assert torch.equal(y[keep], y0[keep])
+    assert bool(torch.isnan(y[1]).all()) and not bool(torch.isfinite(y[[130, T - 1]]).any())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H,E", [(5000, 2048, 160), (16500, 512, 96)])
+def test_router_logits_tiles_in_a_graph(nv, T, H, E, dtype):
+    """Projection and routing captured together, replayed on new inputs and
+    weights, with eager calls between the replays and on another stream."""
+    x, w, b = _gate(T, H, E, dtype, 4)
+    nv.route(nv.router_logits(x, w, bias=b), 4)
+    torch.cuda.synchronize()
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        y = nv.router_logits(x, w, bias=b)
+        ids, wt = nv.route(y, 4)
+    for i in range(3):
+        for dst, src in zip((x, w, b), _gate(T, H, E, dtype, 40 + i)):
+            dst.copy_(src)
+        g.replay()
+        y2 = nv.router_logits(x, w, bias=b)
+        i2, wt2 = nv.route(y2, 4)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            y3 = nv.router_logits(x, w, bias=b)
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(y, y3) and torch.equal(ids, i2) and torch.equal(wt, wt2), i

@@ -125,3 +125,23 @@ def test_route_refuses_outputs_over_its_operands(nv, dtype):
                 assert _route(nv, T=T, E=E, k=k, dtype=dtype, **now) == -1
                 error = nv._lib.nvfp4_last_error()
                 assert b"overlap" in error and name in error
+
+
+def test_router_logits_border_between_slices_and_tiles(nv):
+    """The workspace shows which kernel takes a call: above the bound on the
+    slices' work (32 x 32 tiles times H) the tiles' partial sums, and for fp32
+    weights their three bf16 planes."""
+    size = nv._lib.moe_router_logits_workspace_size
+    H, E = 1024, 256
+    assert size(2048, H, E, 0) == 0 and size(2816, H, E, 1) == 0
+    assert size(2049, H, E, 0) == 2 * 2049 * E * 4
+    assert size(2817, H, E, 1) == 3 * 2817 * E * 4 + 3 * E * H * 2
+    assert size(16387, 512, E, 0) == 0                                        # the kernel stores the result
+    assert size(16387, 512, E, 1) == 3 * 16387 * E * 4 + 3 * E * 512 * 2
+    # the shapes that test the tiled kernel: all of them have fp32 planes
+    for T, H, E in ((16500, 448, 255), (40000, 64, 300), (70001, 576, 4), (4100, 1024, 256), (1100, 7168, 128),
+                    (2100, 4096, 101), (3000, 2048, 512), (8191, 320, 260), (5000, 2048, 160), (5001, 2048, 159),
+                    (20000, 512, 130), (4500, 2048, 160), (16500, 512, 96)):
+        need, planes = size(T, H, E, 1), (3 * E * H * 2 + 255) // 256 * 256
+        parts = (need - planes) // (4 * T * E)
+        assert parts >= 3 and parts % 3 == 0 and need == planes + (parts * T * E * 4 + 255) // 256 * 256, (T, H, E)
