@@ -335,3 +335,27 @@ def test_lora_inner_result_next_to_the_largest_value(nv, T, L, dtype):
     out = nv.lora_add(y, x, a, b, ids)
     assert bool(torch.isfinite(out).all())
     _check(out, y, x, a, b, ids, None)
+
+
+# Outputs so wide and tiles so many that a wave takes several 64-column chunks
+# (from 4096 tiles x 256-column blocks on), with whole and ragged last chunks,
+# by tiles of 16 tokens (up to 256 tokens and for many adapters) and of 64, and
+# every width of r; the last three have one chunk and ranks over 64 in 64-token tiles
+WIDE = [(128, 256, 16384, 16, 64), (256, 128, 16392, 40, 5), (256, 64, 8200, 96, 7), (200, 96, 16392, 128, 3),
+        (600, 64, 16392, 72, 40), (1000, 64, 16504, 24, 60), (4096, 64, 16392, 32, 8), (4096, 64, 16440, 64, 8),
+        (4096, 64, 16392, 72, 8), (2500, 128, 32776, 128, 3), (600, 512, 264, 96, 3), (700, 128, 200, 72, 2),
+        (1000, 320, 520, 128, 4)]
+
+
+@pytest.mark.parametrize("T,K,N,r,L", WIDE)
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_lora_wide(nv, T, K, N, r, L, dtype):
+    p = _problem(T, K, N, r, L, dtype, "mixed", T + r)
+    out = torch.full_like(p[0], 3.0)
+    nv.lora_add(*p[:5], scales=p[5], out=out)
+    _check(out, *p)
+    y = p[0].clone()
+    nv.lora_add(y, *p[1:5], scales=p[5], out=y)
+    assert torch.equal(y, out)
+    p[4].fill_(L - 1)                # one adapter has all tokens
+    _check(nv.lora_add(*p[:5], scales=p[5]), *p)
