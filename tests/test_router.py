@@ -145,3 +145,23 @@ def test_router_logits_border_between_slices_and_tiles(nv):
         need, planes = size(T, H, E, 1), (3 * E * H * 2 + 255) // 256 * 256
         parts = (need - planes) // (4 * T * E)
         assert parts >= 3 and parts % 3 == 0 and need == planes + (parts * T * E * 4 + 255) // 256 * 256, (T, H, E)
+
+
+@pytest.mark.parametrize("kw,beyond", [
+    (dict(T=1 << 24), dict(T=(1 << 24) + 1)), (dict(E=512), dict(E=513)), (dict(k=32), dict(k=33)),
+    (dict(E=512, n_group=64, topk_group=64), dict(E=390, n_group=65, topk_group=65))])
+def test_route_limits(nv, kw, beyond):
+    """The last supported size reaches the check of the pointers, the next one
+    does not."""
+    assert _route(nv, logits=None, **kw) == -1
+    assert b"null pointer" in nv._lib.nvfp4_last_error()
+    assert _route(nv, logits=None, **beyond) == -2
+
+
+@pytest.mark.parametrize("kw,beyond", [
+    (dict(T=1 << 20), dict(T=(1 << 20) + 1)), (dict(E=512), dict(E=513)),
+    (dict(H=1 << 20), dict(H=(1 << 20) + 32)), (dict(H=32), dict(H=16))])
+def test_router_logits_limits(nv, kw, beyond):
+    assert _logits(nv, x=None, **kw) == -1
+    assert b"null pointer" in nv._lib.nvfp4_last_error()
+    assert _logits(nv, x=None, **beyond) == -2
