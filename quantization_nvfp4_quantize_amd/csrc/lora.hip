@@ -343,6 +343,7 @@ struct Terms {
 };
 template <int TERMS>
 __device__ __forceinline__ Terms<TERMS> split(const f32x4& a, const f32x4& b) {
+  constexpr float kMost = 0x1.fep127f;
   float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   Terms<TERMS> t;
 #pragma unroll
@@ -350,10 +351,14 @@ __device__ __forceinline__ Terms<TERMS> split(const f32x4& a, const f32x4& b) {
     bf16x8 h;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float most = 0x1.fep127f, w = __builtin_fabsf(v[i]);
-      h[i] = (__bf16)(w > most && w < INFINITY ? __builtin_copysignf(most, v[i]) : v[i]);
-      const float f = (float)h[i];
-      v[i] = __builtin_fabsf(f) < INFINITY ? v[i] - f : 0.0f;  // not inf - inf
+      if (q == 0) {  // what it leaves is finite and small
+        const bool finite = __builtin_fabsf(v[i]) < INFINITY;
+        h[i] = (__bf16)(finite ? __builtin_amdgcn_fmed3f(v[i], -kMost, kMost) : v[i]);
+        v[i] = finite ? v[i] - (float)h[i] : 0.0f;  // not inf - inf
+      } else {
+        h[i] = (__bf16)v[i];
+        v[i] -= (float)h[i];
+      }
     }
     t.f[q] = __builtin_bit_cast(uint4, h);
   }
