@@ -248,8 +248,9 @@ __global__ __launch_bounds__(64 * kSliceWaves) void gate_slice_kernel(GateParams
 // the next step are read before this step's MFMAs.  Chunk c (16 bytes) of a row
 // lies at c ^ swz_key(row).  The experts are the MFMA's rows, so that a lane
 // ends with four experts of one token in a register quad, which is one store.
-// The direct loads alone (32 KiB a step and CU) take 50 of the 63 us of T16384
-// H7168 E256, 40 when all of them hit the L2.  64 x 128 outputs per wave over
+// The direct loads alone (32 KiB a step and CU) take 48 of the 71 to 75 us of
+// T16384 H7168 E256 on repeated inputs, part of which stay in the 256 MB cache,
+// and 77 of the 80 us on changing ones.  64 x 128 outputs per wave over
 // quarters of a step, a quarter less LDS traffic, gain 1 % there and lose 10 %
 // below 4096 tokens.  The time outside the loop counts as well: an epilogue that
 // sent all sums through LDS and stored single floats took 16000 cycles.
@@ -433,6 +434,11 @@ __global__ __launch_bounds__(256) void gate_sum_kernel(const float* __restrict__
 // (0.57 M) 14.8 / 13.9; H4096 E72 at 1024 (0.39 M) 10.6 / 12.2, at 2048 (0.79 M)
 // 16.8 / 13.2; fp32, whose tiles cost three times as much, H7168 E256 at 384 (0.69
 // M) 20.1 / 23.1, at 512 (0.92 M) 24.7 / 22.6, H4096 E72 at 2048 21.6 / 20.8.
+// The tiles' steps are 64 wide, so that an H of 32 beyond a multiple of 64 goes
+// to the slices at any size, which costs with many tokens: H7136 against H7168
+// (E256, bf16 / fp32) at 1024 tokens 27 / 39 against 20 / 30, at 4096 100 / 133
+// against 30 / 77, at 16384 396 / 522 against 85 / 240 (a product of fp32 copies
+// in the library: 517 / 506).  Padding H with zeros, once in w, avoids it.
 struct GatePlan {
   enum Kind { kDot, kSlice, kTile } kind;
   int slices, parts;
