@@ -270,8 +270,8 @@ def lora_add(y, x, a, b, ids, scales=None, out=None, ws=None):
     y [T][N] bf16 or float32; x bf16 [T][K]: the projection's input; a bf16
     [L][r][K], b bf16 [L][N][r] (smaller ranks padded with zeros); ids int32
     [T]; scales float32 [L].  out: a new tensor by default; pass y to work in
-    place (x's memory is fine, too).  ws: a workspace of lora_add_workspace, not shared by calls that may
-    run at the same time."""
+    place (x's memory is fine, too).  ws: a workspace of lora_add_workspace,
+    not shared by calls that may run at the same time."""
     if y.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"y must be bfloat16 or float32, got {y.dtype}")
     if y.dim() != 2 or x.dim() != 2 or a.dim() != 3:
