@@ -413,6 +413,81 @@ size_t mxfp4_linear_workspace_size(int64_t M, int64_t K, int64_t N);
 int mxfp4_linear(const uint16_t *x, int64_t M, int64_t K, const uint8_t *w_q, const uint8_t *w_scale, int64_t N,
                  int out_dtype, void *out, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * nvfp4_matvec, mxfp4_matvec -- products of a few tokens with 4-bit weights:
+ * the projections' weights (as nvfp4_linear and mxfp4_linear take them) with
+ * activations that stay bf16.
+ *   nvfp4_matvec: y[m][n] = w_gs * sum_k x[m][k] * e2m1(w[n][k]) * sf[n][k/16]
+ *   mxfp4_matvec: y[m][n] = sum_k x[m][k] * e2m1(w[n][k]) * 2^(scale[n][k/32] - 127)
+ * Every weight is held exactly, products are exact, accumulated in fp32 in an
+ * order that depends on the sizes alone; one rounding to the output's type.
+ *   x    bf16 [M][K];  w_q [N][K/2];  w_sf [N][K/16], w_scale [N][K/32] with
+ *        codes up to 252 (beyond, a weight may leave bf16's range)
+ *   out  [M][N], bf16 (out_dtype 0) or fp32 (1); over nothing that the call reads
+ *   M >= 0; K % 32 == 0, any N >= 1; M, K, N at most 2^20 (else
+ *   NVFP4_ERR_UNSUPPORTED).  Made for M up to 64: the weights are read once
+ *   per 64 tokens, which for many tokens is slower than the linears' tiles.
+ *   x, w_q and out 16-byte, the scales 4-byte aligned.  A token with infinite
+ *   or NaN values gets results that are not finite, the others keep theirs.
+ *   No workspace.
+ */
+int nvfp4_matvec(const uint16_t *x, int64_t M, int64_t K, const uint8_t *w_q, const uint8_t *w_sf,
+                 const float *w_gs, int64_t N, int out_dtype, void *out, void *stream);
+int mxfp4_matvec(const uint16_t *x, int64_t M, int64_t K, const uint8_t *w_q, const uint8_t *w_scale, int64_t N,
+                 int out_dtype, void *out, void *stream);
+
+/*
+ * Quantized cache -- rows that are quantized as they are written (the keys,
+ * values or latents of a token) and dequantized as they are read back.  A
+ * cache has n_slots slots of one row each; a row has R elements (all heads of
+ * a token) in blocks of consecutive ones.  Formats:
+ *   0  NVFP4: the bytes of nvfp4_quantize with the supplied gs, R % 16 == 0
+ *   1  MXFP4: the bytes of mxfp4_quantize, R % 32 == 0
+ *   2  MXFP8 (OCP MX v1.0, E4M3 elements): per 32 elements the smallest E8M0
+ *      code c with max|x| <= 448 * 2^(c - 127), clamped to [0, 254] (0 for an
+ *      all-zero block): nothing saturates.  element = x / 2^(c - 127) rounded
+ *      to the nearest E4M3 value, ties to even.  R % 32 == 0
+ */
+typedef struct {
+  void *rows;         /* write: the input, bf16; read: the output, [T][R] */
+  int64_t row_stride; /* write: elements from one input row to the next (>= R,
+                         a multiple of 8: rows may be columns of a wider
+                         matrix); read: not used, the output is contiguous */
+  int64_t R;
+  uint8_t *q;         /* [n_slots][R/2], format 2: [n_slots][R] */
+  uint8_t *s;         /* [n_slots][R/16], formats 1 and 2: [n_slots][R/32] */
+  const float *gs;    /* format 0: device float, the global scale */
+} kv_cache_part;
+
+/*
+ * kv_cache_write -- row t of every part goes to slot slots[t].  Slots outside
+ * [0, n_slots) are skipped (a padded batch), other slots are left as they
+ * were.  A slot that occurs twice in one call holds unspecified bytes after.
+ * kv_cache_read -- row t of every output is what slot slots[t] holds, zeros
+ * where that is outside [0, n_slots).
+ * kv_cache_read_pages -- the same by page table: rows cu_lens[b] ..
+ * cu_lens[b + 1] of the output are the rows of sequence b, in order; row i of
+ * it is in slot pages[b][i / page_size] * page_size + i % page_size.  Rows of
+ * pages outside the table or the cache are zeros; output rows that belong to
+ * no sequence (before cu_lens[0], from cu_lens[B] on) are left as they were.
+ *   parts    one or two (keys and values), R may differ
+ *   out      bf16 (out_dtype 0, rounded to nearest even) or fp32 (1, for the MX
+ *            formats exact): e2m1 * sf * gs as nvfp4_dequantize, element *
+ *            2^(c - 127)
+ *   slots    int32 [T];  pages int32 [B][pages_per_seq];  cu_lens int32
+ *            [B + 1], rising.  All on the device.
+ * T is the number of rows of the inputs or outputs; R <= 2^20 and (T + 1) * R
+ * / 8 <= 2^31 (else NVFP4_ERR_UNSUPPORTED).  rows and q 16-byte aligned.  What
+ * a call writes may lie over nothing else that it touches.  No workspace.
+ */
+int kv_cache_write(int format, const kv_cache_part *parts, int n_parts, int64_t T, const int32_t *slots,
+                   int64_t n_slots, void *stream);
+int kv_cache_read(int format, const kv_cache_part *parts, int n_parts, int64_t T, const int32_t *slots,
+                  int64_t n_slots, int out_dtype, void *stream);
+int kv_cache_read_pages(int format, const kv_cache_part *parts, int n_parts, int64_t T, const int32_t *pages,
+                        int64_t B, int64_t pages_per_seq, int64_t page_size, const int32_t *cu_lens,
+                        int64_t n_slots, int out_dtype, void *stream);
+
 /* Helpers. */
 const char *nvfp4_status_string(int status);
 const char *nvfp4_last_error(void);

@@ -46,6 +46,11 @@ class MoeArgs(ctypes.Structure):
     ]
 
 
+class CachePart(ctypes.Structure):
+    """Mirror of kv_cache_part (include/nvfp4moe.h)."""
+    _fields_ = [("rows", _vp), ("row_stride", _i64), ("R", _i64), ("q", _vp), ("s", _vp), ("gs", _vp)]
+
+
 _SIG = {
     "nvfp4_version": (ctypes.c_int, []),
     "nvfp4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -71,6 +76,13 @@ _SIG = {
     "moe_router_logits": (ctypes.c_int, [_vp, _i64, _i64, _vp, ctypes.c_int, _i64, _vp, _vp, _vp, _sz, _vp]),
     "moe_route": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _i64, ctypes.c_int,
                                  ctypes.c_int, ctypes.c_float, _vp, _vp, _vp, _vp]),
+    "nvfp4_matvec": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _i64, ctypes.c_int, _vp, _vp]),
+    "mxfp4_matvec": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _i64, ctypes.c_int, _vp, _vp]),
+    "kv_cache_write": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(CachePart), ctypes.c_int, _i64, _vp, _i64, _vp]),
+    "kv_cache_read": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(CachePart), ctypes.c_int, _i64, _vp, _i64,
+                                     ctypes.c_int, _vp]),
+    "kv_cache_read_pages": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(CachePart), ctypes.c_int, _i64, _vp, _i64, _i64,
+                                           _i64, _vp, _i64, ctypes.c_int, _vp]),
     "moe_expert_ffn_nvfp4_workspace_size": (_sz, [ctypes.POINTER(MoeArgs)]),
     "moe_expert_ffn_nvfp4": (ctypes.c_int, [ctypes.POINTER(MoeArgs), _vp, _sz, _vp]),
     "moe_expert_ffn_nvfp4_noalloc": (ctypes.c_int, [ctypes.POINTER(MoeArgs), _vp]),
@@ -294,6 +306,181 @@ def lora_add_workspace(T, N, K, r, L, device):
     """A dedicated workspace for nvfp4_lora_add (e.g. for graph capture)."""
     return torch.empty(max(int(_lib.nvfp4_lora_add_workspace_size(T, N, K, r, L)), 256), dtype=torch.uint8,
                        device=device)
+
+
+# ------------------------------------------------------------------ few tokens
+_OUT_CODE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _out_code(dtype):
+    if dtype not in _OUT_CODE:
+        raise ValueError(f"the output must be bfloat16 or float32, got {dtype}")
+    return _OUT_CODE[dtype]
+
+
+def _matvec_operands(x, w_q, w_s, block, out_dtype, out):
+    if x.dim() != 2 or w_q.dim() != 2:
+        raise ValueError(f"x must be [M][K] and w_q [N][K/2], got {tuple(x.shape)} and {tuple(w_q.shape)}")
+    (M, K), N, dev = x.shape, w_q.shape[0], x.device
+    _require_all(dev, (x, torch.bfloat16, (M, K), "x"), (w_q, torch.uint8, (N, K // 2), "w_q"),
+                 (w_s, torch.uint8, (N, K // block), "the scales"))
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    else:
+        _require_all(dev, (out, out.dtype, (M, N), "out"))
+    return M, K, N, dev, out, _out_code(out.dtype)
+
+
+def matvec(x, w_q, w_sf, w_gs, out_dtype=torch.bfloat16, out=None):
+    """Products of a few tokens with NVFP4 weights, the activations kept in bf16:
+    y [M][N] = x @ deq(W)^T (bf16 or float32).  x bf16 [M][K], K % 32 == 0; w_q
+    [N][K/2], w_sf [N][K/16], w_gs float32 [1] as linear takes them, any N.
+    Made for M up to 64 (the weights are read once per 64 tokens)."""
+    M, K, N, dev, out, code = _matvec_operands(x, w_q, w_sf, 16, out_dtype, out)
+    _require_all(dev, (w_gs, torch.float32, (1,), "w_gs"))
+    _launch("nvfp4_matvec", dev, _at(x), M, K, _at(w_q), _at(w_sf), _at(w_gs), N, code, _at(out))
+    return out
+
+
+def mx_matvec(x, w_q, w_sc, out_dtype=torch.bfloat16, out=None):
+    """The same with MXFP4 weights (w_sc [N][K/32] E8M0 codes, as mx_linear)."""
+    M, K, N, dev, out, code = _matvec_operands(x, w_q, w_sc, 32, out_dtype, out)
+    _launch("mxfp4_matvec", dev, _at(x), M, K, _at(w_q), _at(w_sc), N, code, _at(out))
+    return out
+
+
+# ------------------------------------------------------------------ quantized cache
+# format -> (code, elements per scale, elements per byte of q)
+_CACHE = {"nvfp4": (0, 16, 2), "mxfp4": (1, 32, 2), "mxfp8": (2, 32, 1)}
+
+
+def _cache_format(format):
+    if format not in _CACHE:
+        raise ValueError(f"format must be one of {sorted(_CACHE)}, got {format!r}")
+    return _CACHE[format]
+
+
+def cache_empty(n_slots, row_shape, format="mxfp8", device="cuda", gs=None):
+    """A cache of n_slots rows of row_shape (for instance (heads, dim)), all zeros:
+    (q, s), or (q, s, gs) for "nvfp4", whose global scale gs (float32 [1]) is
+    supplied."""
+    code, block, per = _cache_format(format)
+    *lead, dim = row_shape
+    if dim <= 0 or dim % block:
+        raise ValueError(f"{format} rows need a last dimension that is a multiple of {block}, got {dim}")
+    if (gs is None) == (code == 0):
+        raise ValueError("a global scale gs goes with format nvfp4, and with no other")
+    q = torch.zeros((n_slots, *lead, dim // per), dtype=torch.uint8, device=device)
+    s = torch.zeros((n_slots, *lead, dim // block), dtype=torch.uint8, device=device)
+    return (q, s) if gs is None else (q, s, gs)
+
+
+def _cache_part(cache, format, dev):
+    """(q, s, gs, row shape, slots) of one cache, checked."""
+    code, block, per = _cache_format(format)
+    if len(cache) != (3 if code == 0 else 2):
+        raise ValueError("a cache is (q, s), for nvfp4 (q, s, gs)")
+    q, s = cache[0], cache[1]
+    gs = cache[2] if code == 0 else None
+    if q.dim() < 2:
+        raise ValueError("q must be [n_slots][...][bytes]")
+    lead, dim = q.shape[:-1], q.shape[-1] * per
+    _require_all(dev, (q, torch.uint8, q.shape, "q"), (s, torch.uint8, (*lead, dim // block), "s"),
+                 (gs, torch.float32, (1,), "gs"))
+    if dim <= 0 or dim % block:
+        raise ValueError(f"the last dimension must be whole blocks of {block} elements, got {dim}")
+    return q, s, gs, (*lead[1:], dim), lead[0]
+
+
+def _pair(v, cache):
+    """One tensor with its cache, or two of each -> lists, and whether it was one."""
+    one = isinstance(cache[0], torch.Tensor)
+    caches = [cache] if one else list(cache)
+    if not 1 <= len(caches) <= 2:
+        raise ValueError("one cache, or two (keys and values)")
+    tensors = [None] * len(caches) if v is None else [v] if isinstance(v, torch.Tensor) else list(v)
+    if len(tensors) != len(caches):
+        raise ValueError(f"{len(tensors)} tensors for {len(caches)} caches")
+    return tensors, caches, one
+
+
+def _row_stride(t, shape, name):
+    """Elements between the rows of [T][*shape] whose rows are contiguous."""
+    R = 1
+    for k in range(t.dim() - 1, 0, -1):
+        if t.shape[k] != 1 and t.stride(k) != R:
+            raise ValueError(f"the rows of {name} must be contiguous (strides {t.stride()})")
+        R *= t.shape[k]
+    return t.stride(0) if t.shape[0] > 1 else R, R
+
+
+def cache_write(rows, slots, cache, format="mxfp8"):
+    """Quantize rows into a cache: row t goes to slot slots[t] (int32 [T]; slots
+    outside the cache are skipped, a slot may occur once).
+
+    rows: bf16 [T][*row_shape]; each row contiguous, the rows any multiple of 8
+    elements apart (keys and values may be columns of one projection's output).
+    cache: as cache_empty makes it.  rows and cache may also be two of each
+    (keys and values), written in one launch.  format: "nvfp4" (the bytes of
+    quantize with the cache's gs), "mxfp4" (of mx_quantize) or "mxfp8" (E4M3
+    elements, a power of two per 32 at which nothing saturates)."""
+    rows, caches, _ = _pair(rows, cache)
+    dev, T = slots.device, slots.shape[0] if slots.dim() == 1 else -1
+    _require_all(dev, (slots, torch.int32, (T,), "slots"))
+    parts, n_slots = (CachePart * len(rows))(), None
+    for part, x, c in zip(parts, rows, caches):
+        q, s, gs, shape, n = _cache_part(c, format, dev)
+        if x.dtype != torch.bfloat16 or x.device != dev or tuple(x.shape) != (T, *shape):
+            raise ValueError(f"rows must be bfloat16 {[T, *shape]} on {dev}, got {x.dtype} {list(x.shape)} on {x.device}")
+        if n_slots not in (None, n):
+            raise ValueError(f"the caches have {n_slots} and {n} slots")
+        n_slots = n
+        stride, R = _row_stride(x, shape, "rows")
+        part.rows, part.row_stride, part.R = x.data_ptr(), stride, R
+        part.q, part.s, part.gs = q.data_ptr(), s.data_ptr(), _at(gs)
+    _launch("kv_cache_write", dev, _CACHE[format][0], parts, len(rows), T, slots.data_ptr(), n_slots)
+
+
+def _cache_read(name, cache, T, format, out_dtype, out, dev, index):
+    outs, caches, one = _pair(out, cache)
+    parts, n_slots, got = (CachePart * len(caches))(), None, []
+    for part, o, c in zip(parts, outs, caches):
+        q, s, gs, shape, n = _cache_part(c, format, dev)
+        if o is None:
+            o = torch.empty((T, *shape), dtype=out_dtype, device=dev)
+        else:
+            _require_all(dev, (o, out_dtype, (T, *shape), "out"))
+        if n_slots not in (None, n):
+            raise ValueError(f"the caches have {n_slots} and {n} slots")
+        n_slots = n
+        part.rows, part.R = o.data_ptr(), q.numel() // n * _CACHE[format][2] if n else o.numel() // T if T else 32
+        part.q, part.s, part.gs = q.data_ptr(), s.data_ptr(), _at(gs)
+        got.append(o)
+    _launch(name, dev, _CACHE[format][0], parts, len(caches), T, *index, n_slots, _out_code(out_dtype))
+    return got[0] if one else tuple(got)
+
+
+def cache_read(cache, slots, format="mxfp8", out_dtype=torch.bfloat16, out=None):
+    """Rows of a cache, dequantized: [T][*row_shape] (bf16 or float32) with row t
+    from slot slots[t] (int32 [T]), zeros where that is outside the cache.  For
+    two caches (keys and values) a pair.  out: tensor(s) to fill, of out_dtype."""
+    T = slots.shape[0] if slots.dim() == 1 else -1
+    _require_all(slots.device, (slots, torch.int32, (T,), "slots"))
+    return _cache_read("kv_cache_read", cache, T, format, out_dtype, out, slots.device, (slots.data_ptr(),))
+
+
+def cache_read_pages(cache, pages, cu_lens, page_size, total, format="mxfp8", out_dtype=torch.bfloat16, out=None):
+    """The rows of B sequences, one after the other: [total][*row_shape] with rows
+    cu_lens[b] .. cu_lens[b + 1] (int32 [B + 1]) those of sequence b, of which
+    row i is in slot pages[b][i // page_size] * page_size + i % page_size (pages
+    int32 [B][P]).  Rows of pages outside the table or the cache are zeros; rows
+    behind the last sequence are left as they were (new tensors: unset)."""
+    if pages.dim() != 2:
+        raise ValueError("pages must be [B][P]")
+    (B, P), dev = pages.shape, pages.device
+    _require_all(dev, (pages, torch.int32, (B, P), "pages"), (cu_lens, torch.int32, (B + 1,), "cu_lens"))
+    return _cache_read("kv_cache_read_pages", cache, total, format, out_dtype, out, dev,
+                       (pages.data_ptr(), B, P, page_size, cu_lens.data_ptr()))
 
 
 # ------------------------------------------------------------------ MXFP4

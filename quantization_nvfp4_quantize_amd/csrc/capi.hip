@@ -509,6 +509,183 @@ int mxfp4_linear(const uint16_t* x, int64_t M, int64_t K, const uint8_t* w_q, co
                     "mxfp4_linear");
 }
 
+// ------------------------------------------------------------------ few tokens, 4-bit weights
+namespace {
+
+// T and N of a call of few tokens: grid.y counts slices of tokens, and the
+// kernels keep K in 32 bits.
+constexpr int64_t kMaxMatvecDim = (int64_t)1 << 20;
+
+int matvec(const char* name, int fmt, const uint16_t* x, int64_t M, int64_t K, const uint8_t* w_q, const uint8_t* w_s,
+           const float* w_gs, int64_t N, int out_dtype, void* out, void* stream) {
+  g_last_error[0] = 0;
+  if (M < 0 || K <= 0 || N <= 0 || (out_dtype != 0 && out_dtype != 1))
+    return fail(NVFP4_ERR_INVALID_ARG, "%s: need M >= 0, K, N > 0 and out_dtype 0 (bf16) or 1 (fp32)", name);
+  if (K % 32 != 0 || M > kMaxMatvecDim || K > kMaxMatvecDim || N > kMaxMatvecDim)
+    return fail(NVFP4_ERR_UNSUPPORTED, "%s: need K %% 32 == 0 and M, K, N at most 2^20 (M=%lld K=%lld N=%lld)", name,
+                (long long)M, (long long)K, (long long)N);
+  if (M == 0) return NVFP4_OK;
+  if (!x || !w_q || !w_s || !out || (fmt == nvfp4::kNvfp4 && !w_gs))
+    return fail(NVFP4_ERR_INVALID_ARG, "%s: null required pointer", name);
+  if (!aligned(x, 16) || !aligned(w_q, 16) || !aligned(w_s, 4) || !aligned(w_gs, 4) || !aligned(out, 16))
+    return fail(NVFP4_ERR_INVALID_ARG, "%s: x, w_q and out must be 16-byte, the scales 4-byte aligned", name);
+  const int64_t g = fmt == nvfp4::kNvfp4 ? 16 : 32;
+  const Span o = {out, (size_t)(M * N) * (out_dtype == 0 ? 2 : 4), "out"};
+  for (const Span& in : {Span{x, (size_t)(M * K) * 2, "x"}, Span{w_q, (size_t)(N * K / 2), "w_q"},
+                         Span{w_s, (size_t)(N * (K / g)), "w_sf"}, Span{w_gs, 4, "w_gs"}})
+    if (overlap(o, in)) return fail(NVFP4_ERR_INVALID_ARG, "%s: out and %s overlap", name, in.name);
+  return hip_status(nvfp4::launch_matvec(fmt, x, M, (int)K, w_q, w_s, w_gs, N, out_dtype == 0, out,
+                                         reinterpret_cast<hipStream_t>(stream)),
+                    name);
+}
+
+}  // namespace
+
+int nvfp4_matvec(const uint16_t* x, int64_t M, int64_t K, const uint8_t* w_q, const uint8_t* w_sf, const float* w_gs,
+                 int64_t N, int out_dtype, void* out, void* stream) {
+  return matvec("nvfp4_matvec", nvfp4::kNvfp4, x, M, K, w_q, w_sf, w_gs, N, out_dtype, out, stream);
+}
+
+int mxfp4_matvec(const uint16_t* x, int64_t M, int64_t K, const uint8_t* w_q, const uint8_t* w_scale, int64_t N,
+                 int out_dtype, void* out, void* stream) {
+  return matvec("mxfp4_matvec", nvfp4::kMxfp4, x, M, K, w_q, w_scale, nullptr, N, out_dtype, out, stream);
+}
+
+// ------------------------------------------------------------------ quantized cache
+namespace {
+
+struct CacheCall {
+  nvfp4::CachePart part[2];
+  Span q[2], s[2];
+};
+
+// The checks that the three calls share, and the parts as the launchers take
+// them.  rows: the bf16 input of a write, the output of a read (out_bytes per
+// element).
+int cache_parts(const char* name, int format, const kv_cache_part* parts, int n_parts, int64_t T, int64_t n_slots,
+                bool write, CacheCall* c) {
+  g_last_error[0] = 0;
+  if (format < 0 || format > 2 || n_parts < 1 || n_parts > 2 || !parts || T < 0 || n_slots < 0)
+    return fail(NVFP4_ERR_INVALID_ARG, "%s: need format 0, 1 or 2, one or two parts, T >= 0, n_slots >= 0", name);
+  if (n_slots > INT32_MAX) return fail(NVFP4_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 slots", name);
+  const int64_t block = format == nvfp4::kNvfp4 ? 16 : 32;
+  for (int i = 0; i < n_parts; ++i) {
+    const kv_cache_part& a = parts[i];
+    if (a.R <= 0 || a.R % block != 0)
+      return fail(NVFP4_ERR_INVALID_ARG, "%s: rows of %lld elements are no whole blocks of %lld", name, (long long)a.R,
+                  (long long)block);
+    if (a.R > ((int64_t)1 << 20) || T > ((int64_t)1 << 31) / (a.R / 8) - 1)
+      return fail(NVFP4_ERR_UNSUPPORTED, "%s: need R <= 2^20 and (T + 1) * R / 8 <= 2^31", name);
+    if (write && (a.row_stride % 8 != 0 || (T > 1 && a.row_stride < a.R)))
+      return fail(NVFP4_ERR_INVALID_ARG, "%s: row_stride must be a multiple of 8 and at least R", name);
+    if (T > 0 && (!a.rows || (n_slots > 0 && (!a.q || !a.s)) || (format == nvfp4::kNvfp4 && !a.gs)))
+      return fail(NVFP4_ERR_INVALID_ARG, "%s: null required pointer", name);
+    if (!aligned(a.rows, 16) || !aligned(a.q, 16) || !aligned(a.gs, 4))
+      return fail(NVFP4_ERR_INVALID_ARG, "%s: rows and q must be 16-byte aligned", name);
+    c->part[i] = {static_cast<const uint16_t*>(a.rows), a.row_stride, a.rows, a.R, a.q, a.s, a.gs};
+    c->q[i] = {a.q, (size_t)n_slots * (size_t)(format == nvfp4::kMxfp8 ? a.R : a.R / 2), "q"};
+    c->s[i] = {a.s, (size_t)n_slots * (size_t)(a.R / block), "s"};
+  }
+  return NVFP4_OK;
+}
+
+// Everything that a call writes must lie apart from the rest.
+int cache_apart(const char* name, const Span* written, int n_written, const Span* read, int n_read) {
+  for (int i = 0; i < n_written; ++i) {
+    for (int j = i + 1; j < n_written; ++j)
+      if (overlap(written[i], written[j]))
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: %s and %s overlap", name, written[i].name, written[j].name);
+    for (int j = 0; j < n_read; ++j)
+      if (overlap(written[i], read[j]))
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: %s and %s overlap", name, written[i].name, read[j].name);
+  }
+  return NVFP4_OK;
+}
+
+int cache_read_spans(const char* name, const kv_cache_part* parts, int n, int64_t T, int out_dtype, const CacheCall& c,
+                     const Span& a, const Span& b) {
+  Span out[2], in[8];
+  int k = 0;
+  for (int i = 0; i < n; ++i) {
+    out[i] = {parts[i].rows, (size_t)(T * parts[i].R) * (out_dtype == 0 ? 2 : 4), "rows"};
+    in[k++] = c.q[i];
+    in[k++] = c.s[i];
+    in[k++] = {c.part[i].gs, 4, "gs"};
+  }
+  in[k++] = a;
+  in[k++] = b;
+  return cache_apart(name, out, n, in, k);
+}
+
+}  // namespace
+
+int kv_cache_write(int format, const kv_cache_part* parts, int n_parts, int64_t T, const int32_t* slots,
+                   int64_t n_slots, void* stream) {
+  CacheCall c;
+  int st = cache_parts("kv_cache_write", format, parts, n_parts, T, n_slots, true, &c);
+  if (st) return st;
+  if (T > 0 && !slots) return fail(NVFP4_ERR_INVALID_ARG, "kv_cache_write: slots must be non-null");
+  if (!aligned(slots, 4)) return fail(NVFP4_ERR_INVALID_ARG, "kv_cache_write: slots must be 4-byte aligned");
+  if (T == 0 || n_slots == 0) return NVFP4_OK;
+  Span out[4], in[5];
+  int w = 0, r = 0;
+  for (int i = 0; i < n_parts; ++i) {
+    out[w++] = c.q[i];
+    out[w++] = c.s[i];
+    in[r++] = {parts[i].rows, (size_t)((T - 1) * parts[i].row_stride + parts[i].R) * 2, "rows"};
+    in[r++] = {parts[i].gs, 4, "gs"};
+  }
+  in[r++] = {slots, (size_t)T * 4, "slots"};
+  if ((st = cache_apart("kv_cache_write", out, w, in, r))) return st;
+  return hip_status(nvfp4::launch_cache_write(format, c.part, n_parts, T, slots, n_slots,
+                                              reinterpret_cast<hipStream_t>(stream)),
+                    "kv_cache_write");
+}
+
+int kv_cache_read(int format, const kv_cache_part* parts, int n_parts, int64_t T, const int32_t* slots,
+                  int64_t n_slots, int out_dtype, void* stream) {
+  CacheCall c;
+  int st = cache_parts("kv_cache_read", format, parts, n_parts, T, n_slots, false, &c);
+  if (st) return st;
+  if (out_dtype != 0 && out_dtype != 1)
+    return fail(NVFP4_ERR_INVALID_ARG, "kv_cache_read: out_dtype must be 0 (bf16) or 1 (fp32)");
+  if (T > 0 && !slots) return fail(NVFP4_ERR_INVALID_ARG, "kv_cache_read: slots must be non-null");
+  if (!aligned(slots, 4)) return fail(NVFP4_ERR_INVALID_ARG, "kv_cache_read: slots must be 4-byte aligned");
+  if (T == 0) return NVFP4_OK;
+  if ((st = cache_read_spans("kv_cache_read", parts, n_parts, T, out_dtype, c, {slots, (size_t)T * 4, "slots"},
+                             {nullptr, 0, ""})))
+    return st;
+  return hip_status(nvfp4::launch_cache_read(format, c.part, n_parts, T, slots, n_slots, out_dtype == 0,
+                                             reinterpret_cast<hipStream_t>(stream)),
+                    "kv_cache_read");
+}
+
+int kv_cache_read_pages(int format, const kv_cache_part* parts, int n_parts, int64_t T, const int32_t* pages,
+                        int64_t B, int64_t pages_per_seq, int64_t page_size, const int32_t* cu_lens, int64_t n_slots,
+                        int out_dtype, void* stream) {
+  CacheCall c;
+  int st = cache_parts("kv_cache_read_pages", format, parts, n_parts, T, n_slots, false, &c);
+  if (st) return st;
+  if ((out_dtype != 0 && out_dtype != 1) || B < 0 || pages_per_seq < 0 || page_size < 1)
+    return fail(NVFP4_ERR_INVALID_ARG,
+                "kv_cache_read_pages: need out_dtype 0 (bf16) or 1 (fp32), B and pages_per_seq >= 0, page_size >= 1");
+  if (B >= INT32_MAX || pages_per_seq > INT32_MAX || page_size > INT32_MAX)
+    return fail(NVFP4_ERR_UNSUPPORTED, "kv_cache_read_pages: B, pages_per_seq or page_size beyond 2^31 - 1");
+  if (T > 0 && B > 0 && (!cu_lens || (pages_per_seq > 0 && !pages)))
+    return fail(NVFP4_ERR_INVALID_ARG, "kv_cache_read_pages: pages and cu_lens must be non-null");
+  if (!aligned(pages, 4) || !aligned(cu_lens, 4))
+    return fail(NVFP4_ERR_INVALID_ARG, "kv_cache_read_pages: pages and cu_lens must be 4-byte aligned");
+  if (T == 0 || B == 0) return NVFP4_OK;
+  if ((st = cache_read_spans("kv_cache_read_pages", parts, n_parts, T, out_dtype, c,
+                             {pages, (size_t)(B * pages_per_seq) * 4, "pages"},
+                             {cu_lens, (size_t)(B + 1) * 4, "cu_lens"})))
+    return st;
+  return hip_status(nvfp4::launch_cache_read_pages(format, c.part, n_parts, T, pages, B, pages_per_seq, page_size,
+                                                   cu_lens, n_slots, out_dtype == 0,
+                                                   reinterpret_cast<hipStream_t>(stream)),
+                    "kv_cache_read_pages");
+}
+
 // ------------------------------------------------------------------ MoE
 namespace {
 

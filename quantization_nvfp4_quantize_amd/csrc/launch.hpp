@@ -156,6 +156,33 @@ hipError_t launch_lora_add(const void* y, bool bf16, int64_t T, int64_t N, const
                            const uint16_t* a, const uint16_t* b, int r, int L, const int32_t* ids,
                            const float* scales, void* out, void* ws, hipStream_t s);
 
+// ---- matvec.hip
+// y [M][N] = gs * x [M][K] (bf16) @ W^T with 4-bit weights W [N][K] (fmt kNvfp4
+// or kMxfp4, gs null for the latter), K % 32 == 0; y bf16 or fp32.
+enum BlockFormat { kNvfp4 = 0, kMxfp4 = 1, kMxfp8 = 2 };
+hipError_t launch_matvec(int fmt, const uint16_t* x, int64_t M, int K, const uint8_t* w_q, const uint8_t* w_s,
+                         const float* w_gs, int64_t N, bool bf16_out, void* out, hipStream_t s);
+
+// ---- cache.hip
+// One tensor of a cache: rows of R elements (a multiple of 16 for kNvfp4, of
+// 32 for the others; T * R / 8 < 2^31) in slots; gs for kNvfp4 only.
+struct CachePart {
+  const uint16_t* x;  // write: bf16 rows, x_stride elements apart (a multiple of 8)
+  int64_t x_stride;
+  void* out;          // read: [T][R]
+  int64_t R;
+  uint8_t* q;
+  uint8_t* s;
+  const float* gs;
+};
+hipError_t launch_cache_write(int fmt, const CachePart* parts, int n, int64_t T, const int32_t* slots, int64_t n_slots,
+                              hipStream_t s);
+hipError_t launch_cache_read(int fmt, const CachePart* parts, int n, int64_t T, const int32_t* slots, int64_t n_slots,
+                             bool bf16_out, hipStream_t s);
+hipError_t launch_cache_read_pages(int fmt, const CachePart* parts, int n, int64_t T, const int32_t* pages, int64_t B,
+                                   int64_t wide, int64_t page_size, const int32_t* cu_lens, int64_t n_slots,
+                                   bool bf16_out, hipStream_t s);
+
 // ---- mxfp4.hip (OCP MX v1.0 MXFP4: E8M0 scale per 32 elements, E2M1 elements)
 // n bf16 values (n % 32 == 0) -> q [n/2] (element 2i in the low nibble of
 // byte i), sc [n/32] E8M0 codes
