@@ -7,7 +7,9 @@ on the host.  If the shared library has not been built this module raises on
 import -- there is no fallback path.
 """
 import ctypes
+import math
 import os
+import struct
 
 import torch
 
@@ -78,10 +80,10 @@ _SIG = {
                                  ctypes.c_int, ctypes.c_float, _vp, _vp, _vp, _vp]),
     "nvfp4_matvec": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _i64, ctypes.c_int, _vp, _vp]),
     "mxfp4_matvec": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _i64, ctypes.c_int, _vp, _vp]),
-    "kv_cache_write": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(CachePart), ctypes.c_int, _i64, _vp, _i64, _vp]),
-    "kv_cache_read": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(CachePart), ctypes.c_int, _i64, _vp, _i64,
+    "kv_cache_write": (ctypes.c_int, [ctypes.c_int, _vp, ctypes.c_int, _i64, _vp, _i64, _vp]),
+    "kv_cache_read": (ctypes.c_int, [ctypes.c_int, _vp, ctypes.c_int, _i64, _vp, _i64,
                                      ctypes.c_int, _vp]),
-    "kv_cache_read_pages": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(CachePart), ctypes.c_int, _i64, _vp, _i64, _i64,
+    "kv_cache_read_pages": (ctypes.c_int, [ctypes.c_int, _vp, ctypes.c_int, _i64, _vp, _i64, _i64,
                                            _i64, _vp, _i64, ctypes.c_int, _vp]),
     "moe_expert_ffn_nvfp4_workspace_size": (_sz, [ctypes.POINTER(MoeArgs)]),
     "moe_expert_ffn_nvfp4": (ctypes.c_int, [ctypes.POINTER(MoeArgs), _vp, _sz, _vp]),
@@ -318,17 +320,23 @@ def _out_code(dtype):
     return _OUT_CODE[dtype]
 
 
-def _matvec_operands(x, w_q, w_s, block, out_dtype, out):
+def _matvec(name, x, w_q, w_s, w_gs, block, out_dtype, out):
     if x.dim() != 2 or w_q.dim() != 2:
         raise ValueError(f"x must be [M][K] and w_q [N][K/2], got {tuple(x.shape)} and {tuple(w_q.shape)}")
     (M, K), N, dev = x.shape, w_q.shape[0], x.device
     _require_all(dev, (x, torch.bfloat16, (M, K), "x"), (w_q, torch.uint8, (N, K // 2), "w_q"),
-                 (w_s, torch.uint8, (N, K // block), "the scales"))
+                 (w_s, torch.uint8, (N, K // block), "the scales"), (w_gs, torch.float32, (1,), "w_gs"))
     if out is None:
+        code = _out_code(out_dtype)
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
     else:
         _require_all(dev, (out, out.dtype, (M, N), "out"))
-    return M, K, N, dev, out, _out_code(out.dtype)
+        code = _out_code(out.dtype)
+    if block == 16:
+        _launch(name, dev, x.data_ptr(), M, K, w_q.data_ptr(), w_s.data_ptr(), w_gs.data_ptr(), N, code, out.data_ptr())
+    else:
+        _launch(name, dev, x.data_ptr(), M, K, w_q.data_ptr(), w_s.data_ptr(), N, code, out.data_ptr())
+    return out
 
 
 def matvec(x, w_q, w_sf, w_gs, out_dtype=torch.bfloat16, out=None):
@@ -336,17 +344,12 @@ def matvec(x, w_q, w_sf, w_gs, out_dtype=torch.bfloat16, out=None):
     y [M][N] = x @ deq(W)^T (bf16 or float32).  x bf16 [M][K], K % 32 == 0; w_q
     [N][K/2], w_sf [N][K/16], w_gs float32 [1] as linear takes them, any N.
     Made for M up to 64 (the weights are read once per 64 tokens)."""
-    M, K, N, dev, out, code = _matvec_operands(x, w_q, w_sf, 16, out_dtype, out)
-    _require_all(dev, (w_gs, torch.float32, (1,), "w_gs"))
-    _launch("nvfp4_matvec", dev, _at(x), M, K, _at(w_q), _at(w_sf), _at(w_gs), N, code, _at(out))
-    return out
+    return _matvec("nvfp4_matvec", x, w_q, w_sf, w_gs, 16, out_dtype, out)
 
 
 def mx_matvec(x, w_q, w_sc, out_dtype=torch.bfloat16, out=None):
     """The same with MXFP4 weights (w_sc [N][K/32] E8M0 codes, as mx_linear)."""
-    M, K, N, dev, out, code = _matvec_operands(x, w_q, w_sc, 32, out_dtype, out)
-    _launch("mxfp4_matvec", dev, _at(x), M, K, _at(w_q), _at(w_sc), N, code, _at(out))
-    return out
+    return _matvec("mxfp4_matvec", x, w_q, w_sc, None, 32, out_dtype, out)
 
 
 # ------------------------------------------------------------------ quantized cache
@@ -382,36 +385,50 @@ def _cache_part(cache, format, dev):
         raise ValueError("a cache is (q, s), for nvfp4 (q, s, gs)")
     q, s = cache[0], cache[1]
     gs = cache[2] if code == 0 else None
-    if q.dim() < 2:
+    held = q.shape
+    if len(held) < 2:
         raise ValueError("q must be [n_slots][...][bytes]")
-    lead, dim = q.shape[:-1], q.shape[-1] * per
-    _require_all(dev, (q, torch.uint8, q.shape, "q"), (s, torch.uint8, (*lead, dim // block), "s"),
-                 (gs, torch.float32, (1,), "gs"))
-    if dim <= 0 or dim % block:
+    dim = held[-1] * per
+    if dim % block or not dim:
         raise ValueError(f"the last dimension must be whole blocks of {block} elements, got {dim}")
-    return q, s, gs, (*lead[1:], dim), lead[0]
+    _require_all(dev, (q, torch.uint8, held, "q"), (s, torch.uint8, (*held[:-1], dim // block), "s"),
+                 (gs, torch.float32, (1,), "gs"))
+    return q, s, gs, (*held[1:-1], dim), held[0]
 
 
 def _pair(v, cache):
     """One tensor with its cache, or two of each -> lists, and whether it was one."""
     one = isinstance(cache[0], torch.Tensor)
-    caches = [cache] if one else list(cache)
+    caches = [cache] if one else cache
     if not 1 <= len(caches) <= 2:
         raise ValueError("one cache, or two (keys and values)")
-    tensors = [None] * len(caches) if v is None else [v] if isinstance(v, torch.Tensor) else list(v)
+    tensors = [None] * len(caches) if v is None else [v] if isinstance(v, torch.Tensor) else v
     if len(tensors) != len(caches):
         raise ValueError(f"{len(tensors)} tensors for {len(caches)} caches")
     return tensors, caches, one
 
 
-def _row_stride(t, shape, name):
-    """Elements between the rows of [T][*shape] whose rows are contiguous."""
-    R = 1
-    for k in range(t.dim() - 1, 0, -1):
-        if t.shape[k] != 1 and t.stride(k) != R:
+_PART = struct.Struct("QqqQQQ")  # kv_cache_part
+
+
+def _row_stride(t, R, name):
+    """Elements between the rows of [T][...] whose rows of R elements are contiguous."""
+    if t.is_contiguous():
+        return R
+    n = 1
+    for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
+        if size != 1 and stride != n:
             raise ValueError(f"the rows of {name} must be contiguous (strides {t.stride()})")
-        R *= t.shape[k]
-    return t.stride(0) if t.shape[0] > 1 else R, R
+        n *= size
+    return t.stride(0) if t.shape[0] > 1 else R
+
+
+def _slots(slots):
+    T = slots.shape[0] if slots.dim() == 1 else None
+    if T is None:
+        raise ValueError(f"slots must be [T], got {list(slots.shape)}")
+    _require_all(slots.device, (slots, torch.int32, (T,), "slots"))
+    return T
 
 
 def cache_write(rows, slots, cache, format="mxfp8"):
@@ -425,38 +442,36 @@ def cache_write(rows, slots, cache, format="mxfp8"):
     quantize with the cache's gs), "mxfp4" (of mx_quantize) or "mxfp8" (E4M3
     elements, a power of two per 32 at which nothing saturates)."""
     rows, caches, _ = _pair(rows, cache)
-    dev, T = slots.device, slots.shape[0] if slots.dim() == 1 else -1
-    _require_all(dev, (slots, torch.int32, (T,), "slots"))
-    parts, n_slots = (CachePart * len(rows))(), None
-    for part, x, c in zip(parts, rows, caches):
+    T, dev = _slots(slots), slots.device
+    parts, n_slots = b"", None
+    for x, c in zip(rows, caches):
         q, s, gs, shape, n = _cache_part(c, format, dev)
-        if x.dtype != torch.bfloat16 or x.device != dev or tuple(x.shape) != (T, *shape):
+        if x.dtype != torch.bfloat16 or x.shape != (T, *shape) or x.device != dev:
             raise ValueError(f"rows must be bfloat16 {[T, *shape]} on {dev}, got {x.dtype} {list(x.shape)} on {x.device}")
-        if n_slots not in (None, n):
+        if n != n_slots and n_slots is not None:
             raise ValueError(f"the caches have {n_slots} and {n} slots")
-        n_slots = n
-        stride, R = _row_stride(x, shape, "rows")
-        part.rows, part.row_stride, part.R = x.data_ptr(), stride, R
-        part.q, part.s, part.gs = q.data_ptr(), s.data_ptr(), _at(gs)
-    _launch("kv_cache_write", dev, _CACHE[format][0], parts, len(rows), T, slots.data_ptr(), n_slots)
+        n_slots, R = n, math.prod(shape)
+        parts += _PART.pack(x.data_ptr(), _row_stride(x, R, "rows"), R, q.data_ptr(), s.data_ptr(),
+                            0 if gs is None else gs.data_ptr())
+    _launch("kv_cache_write", dev, _CACHE[format][0], parts, len(caches), T, slots.data_ptr(), n_slots)
 
 
 def _cache_read(name, cache, T, format, out_dtype, out, dev, index):
     outs, caches, one = _pair(out, cache)
-    parts, n_slots, got = (CachePart * len(caches))(), None, []
-    for part, o, c in zip(parts, outs, caches):
+    code, parts, n_slots, got = _out_code(out_dtype), b"", None, []
+    for o, c in zip(outs, caches):
         q, s, gs, shape, n = _cache_part(c, format, dev)
         if o is None:
             o = torch.empty((T, *shape), dtype=out_dtype, device=dev)
         else:
             _require_all(dev, (o, out_dtype, (T, *shape), "out"))
-        if n_slots not in (None, n):
+        if n != n_slots and n_slots is not None:
             raise ValueError(f"the caches have {n_slots} and {n} slots")
         n_slots = n
-        part.rows, part.R = o.data_ptr(), q.numel() // n * _CACHE[format][2] if n else o.numel() // T if T else 32
-        part.q, part.s, part.gs = q.data_ptr(), s.data_ptr(), _at(gs)
+        parts += _PART.pack(o.data_ptr(), 0, math.prod(shape), q.data_ptr(), s.data_ptr(),
+                            0 if gs is None else gs.data_ptr())
         got.append(o)
-    _launch(name, dev, _CACHE[format][0], parts, len(caches), T, *index, n_slots, _out_code(out_dtype))
+    _launch(name, dev, _CACHE[format][0], parts, len(caches), T, *index, n_slots, code)
     return got[0] if one else tuple(got)
 
 
@@ -464,8 +479,7 @@ def cache_read(cache, slots, format="mxfp8", out_dtype=torch.bfloat16, out=None)
     """Rows of a cache, dequantized: [T][*row_shape] (bf16 or float32) with row t
     from slot slots[t] (int32 [T]), zeros where that is outside the cache.  For
     two caches (keys and values) a pair.  out: tensor(s) to fill, of out_dtype."""
-    T = slots.shape[0] if slots.dim() == 1 else -1
-    _require_all(slots.device, (slots, torch.int32, (T,), "slots"))
+    T = _slots(slots)
     return _cache_read("kv_cache_read", cache, T, format, out_dtype, out, slots.device, (slots.data_ptr(),))
 
 
