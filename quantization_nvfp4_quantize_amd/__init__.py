@@ -168,8 +168,9 @@ def _require_all(device, *specs):
 def _launch(name, device, *args):
     """Call an entry point (its arguments but the stream) on a device's current
     stream, whatever the current device is."""
-    if torch.cuda.current_device() == device.index:
-        status = getattr(_lib, name)(*args, _stream(device))
+    index = device.index
+    if torch._C._cuda_getDevice() == index:  # half a microsecond less than torch.cuda.current_device()
+        status = getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
             status = getattr(_lib, name)(*args, _stream(device))
