@@ -477,7 +477,7 @@ typedef struct {
  *   slots    int32 [T];  pages int32 [B][pages_per_seq];  cu_lens int32
  *            [B + 1], rising.  All on the device.
  * T is the number of rows of the inputs or outputs; R <= 2^20 and (T + 1) * R
- * / 8 <= 2^31 (else NVFP4_ERR_UNSUPPORTED).  rows and q 16-byte aligned.  What
+ * / 8 <= 2^30 (else NVFP4_ERR_UNSUPPORTED).  rows and q 16-byte aligned.  What
  * a call writes may lie over nothing else that it touches.  No workspace.
  */
 int kv_cache_write(int format, const kv_cache_part *parts, int n_parts, int64_t T, const int32_t *slots,

@@ -3,10 +3,13 @@
 // MXFP8 rows (32 E4M3 elements per E8M0 scale, OCP MX v1.0).
 //
 // A slot holds one row of R elements (all heads of one token); rows are
-// independent, so writing one never touches what another holds.  Work is cut
-// into chunks of 8 elements: a lane loads or stores 16 bytes of bf16, the 2
-// (NVFP4) or 4 (MX) lanes of a block exchange their maxima with DPP, and a
-// block never straddles two rows because R is a multiple of its length.
+// independent, so writing one never touches what another holds.  Writes are cut
+// into chunks of 8 elements: a lane loads 16 bytes of bf16, the 2 (NVFP4) or 4
+// (MX) lanes of a block exchange their maxima with DPP, and a block never
+// straddles two rows because R is a multiple of its length.  Both directions are
+// bound by memory: 5.9 TB/s written into MXFP8 (T16384, keys and values), 6.0
+// read back (a copy of 2 + 2 GiB moves 4.9), with streaming stores for what the
+// call does not read again.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -19,8 +22,6 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kCacheThreads = 256;
-constexpr int kCacheUnroll = 4;  // chunks per thread, all loads in flight at once
-constexpr int kCacheChunks = kCacheThreads * kCacheUnroll;
 
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -78,16 +79,17 @@ __device__ __forceinline__ uint32_t mx8_code(float m) {
   return (uint32_t)max((int)(b >> 23) - 8 + (int)((b & 0x7fffffu) > 0x600000u), 0);
 }
 
-template <int FMT>
+template <int FMT, int UNROLL>
 __global__ __launch_bounds__(kCacheThreads) void cache_write_kernel(CacheParams p) {
+  constexpr int kChunks = kCacheThreads * UNROLL;
   __shared__ float rtab[FMT == kNvfp4 ? 128 : 1];
   const PartParams c = blockIdx.y ? p.part[1] : p.part[0];
-  const uint32_t base = blockIdx.x * kCacheChunks + threadIdx.x;
-  if (blockIdx.x * (uint32_t)kCacheChunks >= c.n8) return;  // the other part has longer rows
-  uint4 w[kCacheUnroll];
-  uint32_t slot[kCacheUnroll], col[kCacheUnroll];
+  const uint32_t base = blockIdx.x * kChunks + threadIdx.x;
+  if (blockIdx.x * (uint32_t)kChunks >= c.n8) return;  // the other part has longer rows
+  uint4 w[UNROLL];
+  uint32_t slot[UNROLL], col[UNROLL];
 #pragma unroll
-  for (int u = 0; u < kCacheUnroll; ++u) {
+  for (int u = 0; u < UNROLL; ++u) {
     const uint32_t i = base + u * kCacheThreads;
     slot[u] = ~0u;
     col[u] = 0;
@@ -106,14 +108,14 @@ __global__ __launch_bounds__(kCacheThreads) void cache_write_kernel(CacheParams 
     __syncthreads();
   }
 #pragma unroll
-  for (int u = 0; u < kCacheUnroll; ++u) {
+  for (int u = 0; u < UNROLL; ++u) {
     const bool on = slot[u] < p.n_slots;  // also false for -1
     const int64_t at = (int64_t)slot[u] * c.r8 + col[u];
     if constexpr (FMT == kNvfp4) {
       uint32_t sf;
       const uint32_t n = quantize_half_block(w[u], E, rtab, &sf);
       if (on) {
-        reinterpret_cast<uint32_t*>(c.q)[at] = n;
+        __builtin_nontemporal_store(n, reinterpret_cast<uint32_t*>(c.q) + at);
         if ((col[u] & 1) == 0) c.s[at >> 1] = (uint8_t)sf;
       }
     } else {
@@ -127,7 +129,7 @@ __global__ __launch_bounds__(kCacheThreads) void cache_write_kernel(CacheParams 
         n = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(n, bf16_lo(d[1]) * r, bf16_hi(d[1]) * r, 1.0f, 1);
         n = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(n, bf16_lo(d[2]) * r, bf16_hi(d[2]) * r, 1.0f, 2);
         n = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(n, bf16_lo(d[3]) * r, bf16_hi(d[3]) * r, 1.0f, 3);
-        if (on) reinterpret_cast<uint32_t*>(c.q)[at] = n;
+        if (on) __builtin_nontemporal_store(n, reinterpret_cast<uint32_t*>(c.q) + at);
       } else {
         u32x2 e;  // |x * r| <= 448: the conversion rounds to nearest even there
 #pragma unroll
@@ -136,11 +138,23 @@ __global__ __launch_bounds__(kCacheThreads) void cache_write_kernel(CacheParams 
           e[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(bf16_lo(d[2 * h + 1]) * r, bf16_hi(d[2 * h + 1]) * r, v,
                                                            true);
         }
-        if (on) reinterpret_cast<u32x2*>(c.q)[at] = e;
+        if (on) __builtin_nontemporal_store(e, reinterpret_cast<u32x2*>(c.q) + at);
       }
       if (on && (col[u] & 3) == 0) c.s[at >> 2] = (uint8_t)code;
     }
   }
+}
+
+// Elements 2 h and 2 h + 1 of a dword of E2M1 nibbles, or of half a dword of E4M3 bytes.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ f32x2 pair_fp4(uint32_t q, int h) {
+  return h == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 0)
+         : h == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 1)
+         : h == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 2)
+                  : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 3);
+}
+__device__ __forceinline__ f32x2 pair_fp8(uint32_t q, int h) {
+  return h ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q, 1.0f, true) : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q, 1.0f, false);
 }
 
 constexpr uint32_t kZeros = 0xffffffffu;  // the row is read as zeros
@@ -166,33 +180,22 @@ __device__ __forceinline__ uint32_t slot_of_row(const CacheParams& p, uint32_t t
   return slot < p.n_slots ? (uint32_t)slot : kZeros;
 }
 
-template <bool BF16_OUT>
-__device__ __forceinline__ void store8(void* out, int64_t i, const float* v) {
-  if constexpr (BF16_OUT) {
-    __bf16 h[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) h[k] = (__bf16)v[k];
-    u32x4 o;
-    __builtin_memcpy(&o, h, 16);
-    reinterpret_cast<u32x4*>(out)[i] = o;
-  } else {
-    float4* o = reinterpret_cast<float4*>(out) + 2 * i;
-    o[0] = make_float4(v[0], v[1], v[2], v[3]);
-    o[1] = make_float4(v[4], v[5], v[6], v[7]);
-  }
-}
-
-// A workgroup's chunks belong to a few consecutive rows: one thread per row
-// finds its slot (a search in cu_lens, a load from the page table), all read
-// it from LDS.
-template <int FMT, bool BF16_OUT>
+// A workgroup's units belong to a few consecutive rows: one thread per row finds
+// its slot (a search in cu_lens, a load from the page table), all read it from
+// LDS.  A unit is what 16 bytes of output hold, 8 bf16 or 4 fp32 elements, so
+// that a store instruction of a wave fills whole lines; then non-temporal
+// stores pay (24 sequences of up to 8192 rows of 576 into bf16: 28.7 us against
+// 39.7; two of them 32 bytes apart per lane into fp32: 95 against 64).
+template <int FMT, bool BF16_OUT, int UNROLL>
 __global__ __launch_bounds__(kCacheThreads) void cache_read_kernel(CacheParams p) {
-  __shared__ uint32_t slots[kCacheChunks / 2 + 2];
+  constexpr int kUnit = BF16_OUT ? 8 : 4, kUnits = kCacheThreads * UNROLL, kPerBlock = (FMT == kNvfp4 ? 16 : 32) / kUnit;
+  __shared__ uint32_t slots[kUnits * kUnit / 16 + 2];  // a row has 16 elements at least
   const PartParams c = blockIdx.y ? p.part[1] : p.part[0];
-  const uint32_t first = blockIdx.x * (uint32_t)kCacheChunks;
-  if (first >= c.n8) return;
-  const uint32_t last = min(first + (uint32_t)kCacheChunks, c.n8) - 1;
-  const uint32_t row0 = divide(first, c.by_r8), rows = divide(last, c.by_r8) - row0 + 1;
+  const uint32_t per_row = c.r8 * (8 / kUnit), n = c.n8 * (8 / kUnit), first = blockIdx.x * (uint32_t)kUnits;
+  if (first >= n) return;
+  const uint32_t last = min(first + (uint32_t)kUnits, n) - 1;
+  const auto row_of = [&](uint32_t i) { return divide(i / (8 / kUnit), c.by_r8); };
+  const uint32_t row0 = row_of(first), rows = row_of(last) - row0 + 1;
   for (uint32_t r = threadIdx.x; r < rows; r += kCacheThreads) {
     uint32_t s;
     if (p.slots) {
@@ -205,57 +208,55 @@ __global__ __launch_bounds__(kCacheThreads) void cache_read_kernel(CacheParams p
   }
   const float g = FMT == kNvfp4 ? c.gs[0] : 1.0f;
   __syncthreads();
-  uint32_t slot[kCacheUnroll], code[kCacheUnroll];
-  u32x2 q[kCacheUnroll];
+  uint32_t slot[UNROLL], code[UNROLL];
+  u32x2 q[UNROLL];
 #pragma unroll
-  for (int u = 0; u < kCacheUnroll; ++u) {
+  for (int u = 0; u < UNROLL; ++u) {
     const uint32_t i = first + threadIdx.x + u * kCacheThreads;
     slot[u] = kSkip;
     code[u] = 0;
     q[u] = u32x2{0, 0};
-    if (i < c.n8) {
-      const uint32_t row = divide(i, c.by_r8), col = i - row * c.r8;
+    if (i < n) {
+      const uint32_t row = row_of(i), col = i - row * per_row;
       slot[u] = slots[row - row0];
       if (slot[u] < kSkip) {
-        const int64_t at = (int64_t)slot[u] * c.r8 + col;
-        code[u] = c.s[at >> (FMT == kNvfp4 ? 1 : 2)];
-        if constexpr (FMT == kMxfp8) q[u] = reinterpret_cast<const u32x2*>(c.q)[at];
-        else q[u][0] = reinterpret_cast<const uint32_t*>(c.q)[at];
+        const int64_t at = (int64_t)slot[u] * per_row + col;
+        code[u] = c.s[at / kPerBlock];
+        if constexpr (FMT == kMxfp8 && BF16_OUT) q[u] = reinterpret_cast<const u32x2*>(c.q)[at];
+        else if constexpr (FMT == kMxfp8 || BF16_OUT) q[u][0] = reinterpret_cast<const uint32_t*>(c.q)[at];
+        else q[u][0] = reinterpret_cast<const uint16_t*>(c.q)[at];
       }
     }
   }
 #pragma unroll
-  for (int u = 0; u < kCacheUnroll; ++u) {
+  for (int u = 0; u < UNROLL; ++u) {
     if (slot[u] == kSkip) continue;
-    float v[8];
-    if constexpr (FMT == kMxfp8) {
+    float v[kUnit];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q[u][h], 1.0f, false);
-        const auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q[u][h], 1.0f, true);
-        v[4 * h] = a[0];
-        v[4 * h + 1] = a[1];
-        v[4 * h + 2] = b[0];
-        v[4 * h + 3] = b[1];
-      }
-    } else {
-      const auto f0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u][0], 1.0f, 0);
-      const auto f1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u][0], 1.0f, 1);
-      const auto f2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u][0], 1.0f, 2);
-      const auto f3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u][0], 1.0f, 3);
-      v[0] = f0[0], v[1] = f0[1], v[2] = f1[0], v[3] = f1[1];
-      v[4] = f2[0], v[5] = f2[1], v[6] = f3[0], v[7] = f3[1];
+    for (int h = 0; h < kUnit / 2; ++h) {
+      const auto e = FMT == kMxfp8 ? pair_fp8(q[u][h / 2], h & 1) : pair_fp4(q[u][0], h);
+      v[2 * h] = e[0];
+      v[2 * h + 1] = e[1];
     }
     if constexpr (FMT == kNvfp4) {
       const float sfd = e4m3_decode_signed(code[u]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = (v[k] * sfd) * g;
+      for (int k = 0; k < kUnit; ++k) v[k] = (v[k] * sfd) * g;
     } else {
       const int e = (int)code[u] - 127;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = ldexpf(v[k], e);
+      for (int k = 0; k < kUnit; ++k) v[k] = ldexpf(v[k], e);
     }
-    store8<BF16_OUT>(c.out, (int64_t)first + threadIdx.x + u * kCacheThreads, v);
+    u32x4 o;
+    if constexpr (BF16_OUT) {
+      __bf16 h[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[k] = (__bf16)v[k];
+      __builtin_memcpy(&o, h, 16);
+    } else {
+      __builtin_memcpy(&o, v, 16);
+    }
+    __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(c.out) + ((int64_t)first + threadIdx.x + u * kCacheThreads));
   }
 }
 
@@ -270,21 +271,46 @@ CacheParams params_of(const CachePart* parts, int n, int64_t T) {
   return p;
 }
 
-dim3 grid_of(const CacheParams& p, int n) {
-  const uint32_t most = std::max(p.part[0].n8, n > 1 ? p.part[1].n8 : 0u);
-  return dim3((most + kCacheChunks - 1) / kCacheChunks, n);
+// Grid for units of `elements` elements, `per` of them per workgroup.
+dim3 grid_of(const CacheParams& p, int n, uint32_t elements, uint32_t per) {
+  const uint32_t most = std::max(p.part[0].n8, n > 1 ? p.part[1].n8 : 0u) * (8 / elements);
+  return dim3((most + per - 1) / per, n);
+}
+
+template <int FMT, bool BF16_OUT, int UNROLL>
+void read_with(const CacheParams& p, int n, hipStream_t s) {
+  const dim3 g = grid_of(p, n, BF16_OUT ? 8 : 4, kCacheThreads * UNROLL);
+  cache_read_kernel<FMT, BF16_OUT, UNROLL><<<g, kCacheThreads, 0, s>>>(p);
+}
+
+// Four units per thread keep enough loads in flight for large reads (24 sequences
+// of up to 8192 rows of 576: 28.5 us against 38.6 with one, 29.6 with two); where
+// that leaves CUs without a workgroup, one (262 rows of 8 x 128, keys and values: 3.35 us against 4.1).
+template <int FMT, bool BF16_OUT>
+void read_as(const CacheParams& p, int n, hipStream_t s) {
+  const dim3 g = grid_of(p, n, BF16_OUT ? 8 : 4, 4 * kCacheThreads);
+  if (g.x * g.y <= 256) read_with<FMT, BF16_OUT, 1>(p, n, s);
+  else read_with<FMT, BF16_OUT, 4>(p, n, s);
 }
 
 template <int FMT>
-void read_as(const CacheParams& p, int n, bool bf16_out, hipStream_t s) {
-  if (bf16_out) cache_read_kernel<FMT, true><<<grid_of(p, n), kCacheThreads, 0, s>>>(p);
-  else cache_read_kernel<FMT, false><<<grid_of(p, n), kCacheThreads, 0, s>>>(p);
+hipError_t read_format(const CacheParams& p, int n, bool bf16_out, hipStream_t s) {
+  if (bf16_out) read_as<FMT, true>(p, n, s);
+  else read_as<FMT, false>(p, n, s);
+  return hipGetLastError();
 }
 
 hipError_t launch_read(int fmt, const CacheParams& p, int n, bool bf16_out, hipStream_t s) {
-  if (fmt == kNvfp4) read_as<kNvfp4>(p, n, bf16_out, s);
-  else if (fmt == kMxfp4) read_as<kMxfp4>(p, n, bf16_out, s);
-  else read_as<kMxfp8>(p, n, bf16_out, s);
+  if (fmt == kNvfp4) return read_format<kNvfp4>(p, n, bf16_out, s);
+  if (fmt == kMxfp4) return read_format<kMxfp4>(p, n, bf16_out, s);
+  return read_format<kMxfp8>(p, n, bf16_out, s);
+}
+
+// Two chunks per thread: T16384, keys and values of 8 x 128 into MXFP8 17.1 us
+// (5.9 TB/s) against 17.9 with one or four.
+template <int FMT>
+hipError_t write_format(const CacheParams& p, int n, hipStream_t s) {
+  cache_write_kernel<FMT, 2><<<grid_of(p, n, 8, 2 * kCacheThreads), kCacheThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -296,11 +322,9 @@ hipError_t launch_cache_write(int fmt, const CachePart* parts, int n, int64_t T,
   CacheParams p = params_of(parts, n, T);
   p.slots = slots;
   p.n_slots = (uint32_t)n_slots;
-  const dim3 g = grid_of(p, n);
-  if (fmt == kNvfp4) cache_write_kernel<kNvfp4><<<g, kCacheThreads, 0, s>>>(p);
-  else if (fmt == kMxfp4) cache_write_kernel<kMxfp4><<<g, kCacheThreads, 0, s>>>(p);
-  else cache_write_kernel<kMxfp8><<<g, kCacheThreads, 0, s>>>(p);
-  return hipGetLastError();
+  if (fmt == kNvfp4) return write_format<kNvfp4>(p, n, s);
+  if (fmt == kMxfp4) return write_format<kMxfp4>(p, n, s);
+  return write_format<kMxfp8>(p, n, s);
 }
 
 hipError_t launch_cache_read(int fmt, const CachePart* parts, int n, int64_t T, const int32_t* slots, int64_t n_slots,

@@ -574,8 +574,8 @@ int cache_parts(const char* name, int format, const kv_cache_part* parts, int n_
     if (a.R <= 0 || a.R % block != 0)
       return fail(NVFP4_ERR_INVALID_ARG, "%s: rows of %lld elements are no whole blocks of %lld", name, (long long)a.R,
                   (long long)block);
-    if (a.R > ((int64_t)1 << 20) || T > ((int64_t)1 << 31) / (a.R / 8) - 1)
-      return fail(NVFP4_ERR_UNSUPPORTED, "%s: need R <= 2^20 and (T + 1) * R / 8 <= 2^31", name);
+    if (a.R > ((int64_t)1 << 20) || T > ((int64_t)1 << 30) / (a.R / 8) - 1)
+      return fail(NVFP4_ERR_UNSUPPORTED, "%s: need R <= 2^20 and (T + 1) * R / 8 <= 2^30", name);
     if (write && (a.row_stride % 8 != 0 || (T > 1 && a.row_stride < a.R)))
       return fail(NVFP4_ERR_INVALID_ARG, "%s: row_stride must be a multiple of 8 and at least R", name);
     if (T > 0 && (!a.rows || (n_slots > 0 && (!a.q || !a.s)) || (format == nvfp4::kNvfp4 && !a.gs)))

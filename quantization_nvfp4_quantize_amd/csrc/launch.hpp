@@ -165,7 +165,7 @@ hipError_t launch_matvec(int fmt, const uint16_t* x, int64_t M, int K, const uin
 
 // ---- cache.hip
 // One tensor of a cache: rows of R elements (a multiple of 16 for kNvfp4, of
-// 32 for the others; T * R / 8 < 2^31) in slots; gs for kNvfp4 only.
+// 32 for the others; T * R / 8 < 2^30) in slots; gs for kNvfp4 only.
 struct CachePart {
   const uint16_t* x;  // write: bf16 rows, x_stride elements apart (a multiple of 8)
   int64_t x_stride;

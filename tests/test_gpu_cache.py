@@ -58,7 +58,8 @@ def _same_values(got, q, s, fmt, gs, dtype):
     assert (np.abs(got - ref) <= tol).all()
 
 
-SHAPES = [(1, (8, 128)), (5, (576,)), (130, (3, 96)), (33, (1, 32)), (257, (2, 64)), (1025, (64,)), (7, (16, 256))]
+SHAPES = [(1, (8, 128)), (5, (576,)), (130, (3, 96)), (33, (1, 32)), (257, (2, 64)), (1025, (64,)), (7, (16, 256)),
+          (4099, (4, 160))]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
