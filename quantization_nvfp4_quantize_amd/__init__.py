@@ -155,10 +155,11 @@ def _ws_bytes(ws, device):
 def _require_all(device, *specs):
     """Each (tensor or None, dtype, shape, name) on the device and contiguous:
     _require in one pass over the tensors of a short call."""
+    index = device.index  # None for host tensors, which get_device() calls -1
     for t, dtype, shape, name in specs:
         if t is None:
             continue
-        if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_cuda or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
             _require(t, dtype, name)
             if t.shape != shape:
                 raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -380,21 +381,25 @@ def cache_empty(n_slots, row_shape, format="mxfp8", device="cuda", gs=None):
 
 
 def _cache_part(cache, format, dev):
-    """(q, s, gs, row shape, slots) of one cache, checked."""
+    """(q, s, pointers to q, s and gs, row shape, slots) of one cache, checked."""
     code, block, per = _cache_format(format)
     if len(cache) != (3 if code == 0 else 2):
         raise ValueError("a cache is (q, s), for nvfp4 (q, s, gs)")
     q, s = cache[0], cache[1]
-    gs = cache[2] if code == 0 else None
     held = q.shape
     if len(held) < 2:
         raise ValueError("q must be [n_slots][...][bytes]")
-    dim = held[-1] * per
+    n, *lead, dim = held
+    dim *= per
     if dim % block or not dim:
         raise ValueError(f"the last dimension must be whole blocks of {block} elements, got {dim}")
-    _require_all(dev, (q, torch.uint8, held, "q"), (s, torch.uint8, (*held[:-1], dim // block), "s"),
+    if code:
+        _require_all(dev, (q, torch.uint8, held, "q"), (s, torch.uint8, (n, *lead, dim // block), "s"))
+        return (q.data_ptr(), s.data_ptr(), 0), (*lead, dim), n
+    gs = cache[2]
+    _require_all(dev, (q, torch.uint8, held, "q"), (s, torch.uint8, (n, *lead, dim // block), "s"),
                  (gs, torch.float32, (1,), "gs"))
-    return q, s, gs, (*held[1:-1], dim), held[0]
+    return (q.data_ptr(), s.data_ptr(), gs.data_ptr()), (*lead, dim), n
 
 
 def _pair(v, cache):
@@ -412,16 +417,14 @@ def _pair(v, cache):
 _PART = struct.Struct("QqqQQQ")  # kv_cache_part
 
 
-def _row_stride(t, R, name):
-    """Elements between the rows of [T][...] whose rows of R elements are contiguous."""
-    if t.is_contiguous():
-        return R
-    n = 1
-    for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
-        if size != 1 and stride != n:
-            raise ValueError(f"the rows of {name} must be contiguous (strides {t.stride()})")
-        n *= size
-    return t.stride(0) if t.shape[0] > 1 else R
+def _rows_of(t, shape):
+    """(elements between the rows of t [T][*shape], elements of a row); each row is contiguous."""
+    R, strides = 1, t.stride()
+    for k in range(len(shape) - 1, -1, -1):
+        if strides[k + 1] != R and shape[k] != 1:
+            raise ValueError(f"each row must be contiguous, got strides {strides}")
+        R *= shape[k]
+    return strides[0] if t.shape[0] > 1 else R, R
 
 
 def _slots(slots):
@@ -446,14 +449,13 @@ def cache_write(rows, slots, cache, format="mxfp8"):
     T, dev = _slots(slots), slots.device
     parts, n_slots = b"", None
     for x, c in zip(rows, caches):
-        q, s, gs, shape, n = _cache_part(c, format, dev)
-        if x.dtype != torch.bfloat16 or x.shape != (T, *shape) or x.device != dev:
+        held, shape, n = _cache_part(c, format, dev)
+        if x.dtype is not torch.bfloat16 or x.shape != (T, *shape) or x.get_device() != dev.index:
             raise ValueError(f"rows must be bfloat16 {[T, *shape]} on {dev}, got {x.dtype} {list(x.shape)} on {x.device}")
         if n != n_slots and n_slots is not None:
             raise ValueError(f"the caches have {n_slots} and {n} slots")
-        n_slots, R = n, math.prod(shape)
-        parts += _PART.pack(x.data_ptr(), _row_stride(x, R, "rows"), R, q.data_ptr(), s.data_ptr(),
-                            0 if gs is None else gs.data_ptr())
+        n_slots = n
+        parts += _PART.pack(x.data_ptr(), *_rows_of(x, shape), *held)
     _launch("kv_cache_write", dev, _CACHE[format][0], parts, len(caches), T, slots.data_ptr(), n_slots)
 
 
@@ -461,7 +463,7 @@ def _cache_read(name, cache, T, format, out_dtype, out, dev, index):
     outs, caches, one = _pair(out, cache)
     code, parts, n_slots, got = _out_code(out_dtype), b"", None, []
     for o, c in zip(outs, caches):
-        q, s, gs, shape, n = _cache_part(c, format, dev)
+        held, shape, n = _cache_part(c, format, dev)
         if o is None:
             o = torch.empty((T, *shape), dtype=out_dtype, device=dev)
         else:
@@ -469,8 +471,7 @@ def _cache_read(name, cache, T, format, out_dtype, out, dev, index):
         if n != n_slots and n_slots is not None:
             raise ValueError(f"the caches have {n_slots} and {n} slots")
         n_slots = n
-        parts += _PART.pack(o.data_ptr(), 0, math.prod(shape), q.data_ptr(), s.data_ptr(),
-                            0 if gs is None else gs.data_ptr())
+        parts += _PART.pack(o.data_ptr(), 0, math.prod(shape), *held)
         got.append(o)
     _launch(name, dev, _CACHE[format][0], parts, len(caches), T, *index, n_slots, code)
     return got[0] if one else tuple(got)
