@@ -320,17 +320,28 @@ __global__ __launch_bounds__(64 * kFewWaves, OCC) void matvec_few_kernel(MatvecP
   }
 }
 
-// ---- 9 to 64 tokens per slice: ROWS rows of W per workgroup and the tokens in
+// ---- up to 64 tokens per slice: ROWS rows of W per workgroup and the tokens in
 // MT tiles of 16, both operands streamed into LDS in chunks of 256 k, two
 // chunks ahead, and read from there by the wave that needs them: the waves
 // share the rows by 32 (or 16) and a chunk's eight blocks of 32 k.
-constexpr int kTileK = 256, kTileStages = 3, kTileWaves = 8;
+//
+// Bound by what a CU does per chunk rather than by memory (M64 K4096 N16384: 19.3 us NVFP4,
+// 15.6 MXFP4; loads alone 12.6 and 11.6, and the same without the loads in the
+// loop 17.3 and 13.2): a conversion and two multiplications per pair of NVFP4
+// weights beside the MFMAs, which share the issue slots of a SIMD (16 MFMAs
+// and 64 VALU instructions take about what both take by themselves), the
+// fragments' way out of LDS, a barrier.  Two waves per SIMD instead of four:
+// 20.6 and 16.6.  Measured and not kept: conversions spread between the MFMAs
+// by hand, fragments read a chunk ahead, x and W loaded by different waves with
+// W four chunks ahead (each 0 to 15 % slower); chunks in another order per
+// workgroup (3 % slower).
+constexpr int kTileK = 256, kTileStages = 3;
 constexpr int kTileSeg = 32;  // chunks whose scales are in LDS at a time
 
-template <int FMT, int MT, int ROWS>
-__global__ __launch_bounds__(64 * kTileWaves, 2) void matvec_tile_kernel(MatvecParams p) {
+template <int FMT, int MT, int ROWS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES / 4) void matvec_tile_kernel(MatvecParams p) {
   constexpr int kBlock = FMT == kNvfp4 ? 16 : 32;
-  constexpr int U = ROWS >= 32 ? 2 : 1, RG = ROWS / (16 * U), KS = kTileWaves / RG, JB = 8 / KS;  // row tiles of a wave, row groups, shares of k, blocks of one
+  constexpr int U = ROWS >= 32 ? 2 : 1, RG = ROWS / (16 * U), KS = WAVES / RG, JB = 8 / KS;  // row tiles of a wave, row groups, shares of k, blocks of one
   constexpr int kXChunks = 16 * MT * 32, kStage = kXChunks + ROWS * 8;  // 16-byte chunks
   extern __shared__ u32x4 lds[];
   uint32_t* scales = reinterpret_cast<uint32_t*>(lds + kTileStages * kStage);
@@ -348,30 +359,32 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void matvec_tile_kernel(MatvecP
   // piece q at q ^ (r % 16); then W's rows eight at a time, 8 pieces of 32 k
   // each, in the order 0 8 1 9 .. of their 16, row n's piece q at q ^ (n % 8).
   // Rows in that order and places: every fragment read spreads over all banks.
-  uint32_t xo[MT];
+  constexpr int kXLoads = (8 * MT + WAVES - 1) / WAVES;
+  uint32_t xo[kXLoads];
 #pragma unroll
-  for (int k = 0; k < MT; ++k) {
-    const int r = 2 * (wave + k * kTileWaves) + (lane >> 5);
+  for (int k = 0; k < kXLoads; ++k) {
+    const int r = 2 * (wave + k * WAVES) + (lane >> 5);
     xo[k] = (uint32_t)min(r, tokens - 1) * (uint32_t)(2 * p.K) + 16 * ((lane & 31) ^ (r & 15));
   }
   const int slot = 8 * (wave & 1) + (lane >> 3), row = 16 * (wave >> 1) + (slot >> 1) + 8 * (slot & 1);
   const uint32_t wo = (uint32_t)min(row, rows - 1) * (uint32_t)(p.K / 2) + 16 * ((lane & 7) ^ (row & 7));
-  const bool loads_w = ROWS == 64 || wave < ROWS / 8;  // wave-uniform
+  const bool loads_w = wave < ROWS / 8;  // wave-uniform
   auto issue = [&](int c, int stage) {
     u32x4* st = lds + stage * kStage + 64 * wave;
     if ((c + 1) * kTileK <= p.K) {
 #pragma unroll
-      for (int k = 0; k < MT; ++k)
-        dma16s(reinterpret_cast<f16x8*>(st + 64 * k * kTileWaves), xb + (size_t)c * (2 * kTileK), xo[k]);
+      for (int k = 0; k < kXLoads; ++k)
+        if (wave + k * WAVES < 8 * MT) dma16s(reinterpret_cast<f16x8*>(st + 64 * k * WAVES), xb + (size_t)c * (2 * kTileK), xo[k]);
       if (loads_w) dma16s(reinterpret_cast<f16x8*>(st + kXChunks), wq + (size_t)c * (kTileK / 2), wo);
     } else {
       // pieces behind the row's end: the row's first one instead, their products
       // are left out.  (An offset holds 16 times its piece: never negative.)
       const uint32_t left = (uint32_t)(p.K - c * kTileK);
 #pragma unroll
-      for (int k = 0; k < MT; ++k) {
-        const uint32_t piece = (lane & 31) ^ ((2 * (wave + k * kTileWaves) + (lane >> 5)) & 15);
-        dma16s(reinterpret_cast<f16x8*>(st + 64 * k * kTileWaves), xb,
+      for (int k = 0; k < kXLoads; ++k) {
+        if (wave + k * WAVES >= 8 * MT) break;  // wave-uniform
+        const uint32_t piece = (lane & 31) ^ ((2 * (wave + k * WAVES) + (lane >> 5)) & 15);
+        dma16s(reinterpret_cast<f16x8*>(st + 64 * k * WAVES), xb,
                8 * piece < left ? xo[k] + (uint32_t)c * (2 * kTileK) : xo[k] - 16 * piece);
       }
       const uint32_t piece = (lane & 7) ^ (row & 7);
@@ -387,7 +400,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void matvec_tile_kernel(MatvecP
   auto stage_scales = [&](int seg) {
     const int i = 2 * seg + lane;
     if (i < total)
-      stage_step<FMT, ROWS / kTileWaves>(ws + (size_t)i * (kMvStep / kBlock), wave, kTileWaves, rows, p.K / kBlock,
+      stage_step<FMT, ROWS / WAVES>(ws + (size_t)i * (kMvStep / kBlock), wave, WAVES, rows, p.K / kBlock,
                                          i < full ? 4 : rest, scales + lane * kUnit<FMT>, pitch);
   };
 
@@ -442,14 +455,16 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void matvec_tile_kernel(MatvecP
     }
   };
 
+  const int mine = (8 * MT - wave + WAVES - 1) / WAVES + loads_w;  // loads of this wave and a chunk
   issue(0, 0);
   if (chunks > 1) issue(1, 1);
   stage_scales(0);
   for (int c = 0, stage = 0; c < chunks; ++c) {
     // chunk c has landed, c + 1 may be on its way
     if (c + 1 == chunks) wait_vmcnt<0>();
-    else if (loads_w) wait_vmcnt<MT + 1>();
-    else wait_vmcnt<MT>();
+    else if (mine == kXLoads + 1) wait_vmcnt<kXLoads + 1>();
+    else if (mine == kXLoads) wait_vmcnt<kXLoads>();
+    else wait_vmcnt<kXLoads - 1>();
     lds_barrier();  // for every wave, and every wave has read chunk c - 1
     if (c && c % kTileSeg == 0) {
       stage_scales(c);
@@ -472,8 +487,8 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void matvec_tile_kernel(MatvecP
     for (int u = 0; u < U; ++u) red[((ks * MT + t) * kTiles + U * rg + u) * 64 + lane] = acc[t][u];
   __syncthreads();
 #pragma unroll
-  for (int h = 0; h < (kSums + 64 * kTileWaves - 1) / (64 * kTileWaves); ++h) {
-    const int i = tid + h * 64 * kTileWaves;
+  for (int h = 0; h < (kSums + 64 * WAVES - 1) / (64 * WAVES); ++h) {
+    const int i = tid + h * 64 * WAVES;
     if (i >= kSums) break;
     f32x4 v = red[i];
 #pragma unroll
@@ -484,14 +499,14 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void matvec_tile_kernel(MatvecP
   }
 }
 
-template <int FMT, int MT, int ROWS>
+template <int FMT, int MT, int ROWS, int WAVES>
 void launch_tile(const MatvecParams& p, hipStream_t s) {
   const dim3 g((unsigned)((p.N + ROWS - 1) / ROWS), (unsigned)((p.M + 16 * MT - 1) / (16 * MT)));
   const int total = (p.K + kMvStep - 1) / kMvStep;
-  constexpr int kStages = kTileStages * (16 * MT * 32 + ROWS * 8);
-  static_assert(kStages >= kTileWaves / (ROWS > 32 ? 2 : 1) * MT * ROWS * 4, "the sums take the stages' place");
-  const size_t lds = 16 * (size_t)kStages + 4 * (size_t)ROWS * (std::min(total, 2 * kTileSeg) | 1) * kUnit<FMT>;
-  matvec_tile_kernel<FMT, MT, ROWS><<<g, 64 * kTileWaves, lds, s>>>(p);
+  constexpr int kStages = kTileStages * (16 * MT * 32 + ROWS * 8), kSums = WAVES / (ROWS > 32 ? 2 : 1) * MT * ROWS * 4;
+  const size_t scales = 4 * (size_t)ROWS * (std::min(total, 2 * kTileSeg) | 1) * kUnit<FMT>;
+  const size_t lds = std::max(16 * (size_t)kStages + scales, 16 * (size_t)kSums);  // the sums take the others' place
+  matvec_tile_kernel<FMT, MT, ROWS, WAVES><<<g, 64 * WAVES, lds, s>>>(p);
 }
 
 // Workgroups that the device runs at once, one per CU.
@@ -499,14 +514,14 @@ constexpr int64_t kCus = 256;
 
 // The smallest tile with which every workgroup has a CU of its own: all of them
 // read all of x, so more than one on a CU costs what a larger tile saves, and
-// with fewer rows a workgroup is done sooner (M64 K4096: N4096 11.4, 12.6 and
+// with fewer rows a workgroup is done sooner (NVFP4 M64 K4096: N4096 11.4, 12.6 and
 // 17.6 us with 16, 32 and 64 rows, N8192 20.8, 13.0 and 17.8, N16384 39.6, 24.0 and 18.6).
 template <int FMT, int MT>
 void launch_tiles(const MatvecParams& p, hipStream_t s) {
   const int64_t slices = (p.M + 16 * MT - 1) / (16 * MT);
-  if ((p.N + 15) / 16 * slices <= kCus) launch_tile<FMT, MT, 16>(p, s);
-  else if ((p.N + 31) / 32 * slices <= kCus) launch_tile<FMT, MT, 32>(p, s);
-  else launch_tile<FMT, MT, 64>(p, s);
+  if ((p.N + 15) / 16 * slices <= kCus) launch_tile<FMT, MT, 16, 8>(p, s);
+  else if ((p.N + 31) / 32 * slices <= kCus) launch_tile<FMT, MT, 32, 8>(p, s);
+  else launch_tile<FMT, MT, 64, 16>(p, s);
 }
 
 template <int FMT, bool DIAG, int XR, int NT, int OCC>
@@ -545,7 +560,7 @@ void launch_format(const MatvecParams& p, hipStream_t s) {
     if (rows16 <= 2 * kCus) launch_few<FMT, false, 4, 1, 4>(p, s);
     else launch_few<FMT, false, 4, 2, 4>(p, s);
   } else if (p.M <= 16) {
-    launch_tile<FMT, 1, 64>(p, s);
+    launch_tile<FMT, 1, 64, 8>(p, s);
   } else if (p.M <= 32) {
     launch_tiles<FMT, 2>(p, s);
   } else if (p.M <= 48) {
