@@ -355,7 +355,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void matvec_tile_kernel(Matv
   const int chunks = (p.K + kTileK - 1) / kTileK;
 
   // This lane's sources.  A stage is filled a KiB per load, wave w loads w, w +
-  // 8 ..: first token rows two at a time, 32 pieces of 8 k each, token row r's
+  // WAVES ..: first token rows two at a time, 32 pieces of 8 k each, token row r's
   // piece q at q ^ (r % 16); then W's rows eight at a time, 8 pieces of 32 k
   // each, in the order 0 8 1 9 .. of their 16, row n's piece q at q ^ (n % 8).
   // Rows in that order and places: every fragment read spreads over all banks.

@@ -66,6 +66,51 @@ def test_matvec_against_64_bits(nv, fmt, M, K, N, dtype):
     _check(y, x @ w.T, np.abs(x) @ np.abs(w).T, K, dtype)
 
 
+# sizes on both sides of every choice of a kernel: many rows, and rows longer
+# than the scales that are staged at a time, with a rest behind whole steps
+WIDE = [(1, 288, 12289), (3, 288, 16383), (2, 96, 16500), (4, 160, 28700), (6, 288, 12301), (8, 160, 16384),
+        (7, 288, 16385), (8, 96, 24600), (9, 288, 8190), (12, 288, 8200), (16, 160, 16001), (13, 288, 16400),
+        (20, 288, 4097), (30, 352, 8200), (47, 288, 8191), (40, 160, 8193), (64, 480, 5000), (64, 288, 8200),
+        (50, 544, 16390), (100, 288, 2100), (130, 32, 6000),
+        (1, 17056, 40), (3, 33184, 33), (8, 17056, 18), (6, 20000, 66), (16, 17088, 20), (11, 32800, 5),
+        (20, 8352, 30), (40, 16800, 17), (64, 8320, 50), (33, 24672, 9), (1, 2 ** 20, 3), (64, 2 ** 20, 2)]
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("M,K,N", WIDE)
+def test_matvec_many_and_long_rows(nv, fmt, M, K, N):
+    rng = np.random.Generator(np.random.PCG64(M + 7 * K + N))
+    bits, x = _x_bits(rng, M, K)
+    q, s = weights(rng, N, K, fmt)
+    g = np.float32(0.37) if fmt == "nvfp4" else np.float32(1)
+    w = values(q, s, fmt, g)
+    y = _run(nv, fmt, dev_bf16(bits), _dev(q), _dev(s), _gs(g), torch.float32)
+    _check(y, x @ w.T, np.abs(x) @ np.abs(w).T, K, torch.float32)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("M,K", [(10, 8480), (40, 8480), (12, 16544)])
+def test_matvec_long_and_many_rows(nv, fmt, M, K):
+    """The 64-row tiles with more than one part of the scales: a few rows of
+    many against 64 bits, and every row against the same rows by themselves."""
+    N = 16500
+    gen = torch.Generator(device="cuda:0")
+    gen.manual_seed(K + M)
+    lo, hi, block = (0x20, 0x50, 16) if fmt == "nvfp4" else (118, 126, 32)
+    q = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda:0", generator=gen)
+    s = torch.randint(lo, hi, (N, K // block), dtype=torch.uint8, device="cuda:0", generator=gen)
+    x = torch.randn(M, K, device="cuda:0", generator=gen).bfloat16()
+    y = _run(nv, fmt, x, q, s, _gs(1.0), torch.float32)
+    at = torch.tensor([0, 17, 63, 64, 8191, 16383, 16384, 16447, N - 1], device="cuda:0")
+    w = values(q[at].cpu().numpy(), s[at].cpu().numpy(), fmt)
+    xd = x.double().cpu().numpy()
+    mag = np.abs(xd) @ np.abs(w).T
+    _check(y[:, at], xd @ w.T, mag, K, torch.float32)
+    for n in range(0, N, 4000):  # other kernels, other orders of the same sums
+        part = _run(nv, fmt, x, q[n:n + 4000], s[n:n + 4000], _gs(1.0), torch.float32)
+        assert float((part - y[:, n:n + 4000]).abs().max()) <= 4 * (K + 2) * 2.0 ** -24 * float(mag.max())
+
+
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("M,K,N", [(1, 7168, 300), (4, 1376, 77), (6, 992, 130), (16, 2048, 65), (24, 4096, 48),
                                    (64, 1120, 35)])
@@ -182,6 +227,34 @@ def test_matvec_streams_and_graphs(nv):
         torch.cuda.synchronize()
         for c, y in zip(cases, outs):
             assert torch.equal(y, _run(nv, *c, torch.float32)), r
+
+
+def test_matvec_two_graphs_on_two_streams(nv):
+    """Two captured calls of each kernel, replayed side by side: nothing is shared."""
+    rng = np.random.Generator(np.random.PCG64(14))
+    weight = weights(rng, 5000, 1056, "nvfp4")
+    q, s = (_dev(a) for a in weight)
+    gs = _gs(0.75)
+    streams, graphs, outs, xs = [torch.cuda.Stream() for _ in range(2)], [], [], []
+    for i in range(2):
+        xs.append([dev_bf16(_x_bits(rng, M, 1056)[0]) for M in (2, 7, 15, 30, 64)])
+        graphs.append(torch.cuda.CUDAGraph())
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graphs[i], stream=streams[i]):
+            outs.append([nv.matvec(x, q, s, gs) for x in xs[i]])
+    ref = [[nv.matvec(x, q, s, gs) for x in xs[i]] for i in range(2)]
+    for _ in range(3):
+        for i in range(2):
+            for y in outs[i]:
+                y.zero_()
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert all(torch.equal(a, b) for a, b in zip(outs[i], ref[i]))
 
 
 def test_matvec_weights_beyond_4_gib(nv):
