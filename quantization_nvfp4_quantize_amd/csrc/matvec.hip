@@ -132,8 +132,10 @@ __device__ __forceinline__ void stage_step(const uint8_t* src, int row, int row_
 // (one per token) hold the k's of lane row i and zeros elsewhere: the lanes of
 // lane row i then get the products of their own weights alone, a block's sum
 // per token, and multiply it by their own block's scale -- the weights go into
-// the MFMA unscaled, one conversion for two of them instead of four instructions
-// (one token, N16384: 9.5 us against 11.4).
+// the MFMA without it, one conversion for two of them instead of four instructions
+// (one token, N16384: 9.5 us against 11.4).  They go in 2^-8 times their value,
+// and the scales come with 2^8: 16 products of up to 6 x stay finite where x is,
+// and every product is a multiple of 2^-142, which the sums hold.
 // Else (16 tokens, of which 4 XR are staged): lane rows exchange dwords so that
 // an MFMA takes 32 consecutive k, and the weights are scaled before it.
 constexpr int kFewWaves = 8;
@@ -209,10 +211,10 @@ __global__ __launch_bounds__(64 * kFewWaves, OCC) void matvec_few_kernel(MatvecP
       for (int u = 0; u < NT; ++u) {
         // the lane's two scales are 16 bits of the row's 8 bytes
         const uint32_t s = reinterpret_cast<const uint16_t*>(scales + (16 * u + col) * pitch + step * 2)[part];
-        const float sc[2] = {__builtin_amdgcn_cvt_f32_fp8(s, 0), __builtin_amdgcn_cvt_f32_fp8(s, 1)};
+        const auto sc = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(s, 256.0f, false);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const bf16x8 b0 = weights8<kMxfp4>(g.w[u][2 * h], 1.0f), b1 = weights8<kMxfp4>(g.w[u][2 * h + 1], 1.0f);
+          const bf16x8 b0 = weights8<kMxfp4>(g.w[u][2 * h], 0x1p-8f), b1 = weights8<kMxfp4>(g.w[u][2 * h + 1], 0x1p-8f);
 #pragma unroll
           for (int t = 0; t < XR; ++t) {
             const f32x4 v = mfma16(a[t][2 * h + 1], b1, mfma16(a[t][2 * h], b0, f32x4{0, 0, 0, 0}));

@@ -229,6 +229,28 @@ def test_matvec_streams_and_graphs(nv):
             assert torch.equal(y, _run(nv, *c, torch.float32)), r
 
 
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("M", [1, 4, 7, 16, 40])
+def test_matvec_largest_and_smallest_values(nv, fmt, M):
+    """Activations next to bf16's limit under scales that bring the results back
+    into range, and subnormal ones: nothing overflows or is lost on the way."""
+    rng = np.random.Generator(np.random.PCG64(M))
+    K, N = 1184, 50
+    q, _ = weights(rng, N, K, fmt)
+    sign = (rng.integers(0, 2, (M, K)) << 15).astype(np.uint16)
+    big = (0x7f00 | rng.integers(0, 128, (M, K), dtype=np.uint16) | sign) * (rng.integers(0, 64, (M, K)) == 5).astype(np.uint16)
+    small = rng.integers(0, 0x300, (M, K), dtype=np.uint16) | sign
+    # E4M3 scales of 2^-9 to 3 * 2^-9 and of 16 to 448, E8M0 of 2^-27 to 2^-10 and of 2^3 to 2^12
+    for bits, codes in ((big, (1, 4) if fmt == "nvfp4" else (100, 118)), (small, (0x58, 0x7f) if fmt == "nvfp4" else (130, 140))):
+        s = rng.integers(*codes, (N, K // (16 if fmt == "nvfp4" else 32)), dtype=np.uint8)
+        x = torch.from_numpy(bits.view(np.int16)).view(torch.bfloat16).double().numpy()
+        w = values(q, s, fmt)
+        ref, mag = x @ w.T, np.abs(x) @ np.abs(w).T
+        assert mag.max() < 2.0 ** 128
+        got = _run(nv, fmt, dev_bf16(bits), _dev(q), _dev(s), _gs(1.0), torch.float32).double().cpu().numpy()
+        assert (np.abs(got - ref) <= (K + 2) * (2.0 ** -24 * mag + 2.0 ** -149)).all()
+
+
 def test_matvec_two_graphs_on_two_streams(nv):
     """Two captured calls of each kernel, replayed side by side: nothing is shared."""
     rng = np.random.Generator(np.random.PCG64(14))
