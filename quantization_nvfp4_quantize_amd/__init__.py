@@ -380,25 +380,27 @@ def cache_empty(n_slots, row_shape, format="mxfp8", device="cuda", gs=None):
     return (q, s) if gs is None else (q, s, gs)
 
 
-def _cache_part(cache, format, dev):
-    """(q, s, pointers to q, s and gs, row shape, slots) of one cache, checked."""
-    code, block, per = _cache_format(format)
-    if len(cache) != (3 if code == 0 else 2):
+def _cache_part(cache, form, dev):
+    """(pointers to q, s and gs, row shape, slots) of one cache, checked.  (One
+    condition over both tensors: half of what _require_all takes for them.)"""
+    code, block, per = form
+    if len(cache) != (2 if code else 3):
         raise ValueError("a cache is (q, s), for nvfp4 (q, s, gs)")
     q, s = cache[0], cache[1]
-    held = q.shape
-    if len(held) < 2:
+    if q.dim() < 2:
         raise ValueError("q must be [n_slots][...][bytes]")
-    n, *lead, dim = held
+    n, *lead, dim = q.shape
     dim *= per
     if dim % block or not dim:
         raise ValueError(f"the last dimension must be whole blocks of {block} elements, got {dim}")
+    index = dev.index
+    if (q.dtype is not torch.uint8 or s.dtype is not torch.uint8 or s.shape != (n, *lead, dim // block)
+            or q.get_device() != index or s.get_device() != index or not q.is_contiguous() or not s.is_contiguous()):
+        _require_all(dev, (q, torch.uint8, q.shape, "q"), (s, torch.uint8, (n, *lead, dim // block), "s"))
     if code:
-        _require_all(dev, (q, torch.uint8, held, "q"), (s, torch.uint8, (n, *lead, dim // block), "s"))
         return (q.data_ptr(), s.data_ptr(), 0), (*lead, dim), n
     gs = cache[2]
-    _require_all(dev, (q, torch.uint8, held, "q"), (s, torch.uint8, (n, *lead, dim // block), "s"),
-                 (gs, torch.float32, (1,), "gs"))
+    _require_all(dev, (gs, torch.float32, (1,), "gs"))
     return (q.data_ptr(), s.data_ptr(), gs.data_ptr()), (*lead, dim), n
 
 
@@ -419,6 +421,9 @@ _PART = struct.Struct("QqqQQQ")  # kv_cache_part
 
 def _rows_of(t, shape):
     """(elements between the rows of t [T][*shape], elements of a row); each row is contiguous."""
+    if t.is_contiguous():
+        R = math.prod(shape)
+        return R, R
     R, strides = 1, t.stride()
     for k in range(len(shape) - 1, -1, -1):
         if strides[k + 1] != R and shape[k] != 1:
@@ -428,11 +433,11 @@ def _rows_of(t, shape):
 
 
 def _slots(slots):
-    T = slots.shape[0] if slots.dim() == 1 else None
-    if T is None:
+    if slots.dim() != 1:
         raise ValueError(f"slots must be [T], got {list(slots.shape)}")
-    _require_all(slots.device, (slots, torch.int32, (T,), "slots"))
-    return T
+    if slots.dtype is not torch.int32 or not slots.is_cuda or not slots.is_contiguous():
+        _require(slots, torch.int32, "slots")
+    return len(slots)
 
 
 def cache_write(rows, slots, cache, format="mxfp8"):
@@ -446,24 +451,25 @@ def cache_write(rows, slots, cache, format="mxfp8"):
     quantize with the cache's gs), "mxfp4" (of mx_quantize) or "mxfp8" (E4M3
     elements, a power of two per 32 at which nothing saturates)."""
     rows, caches, _ = _pair(rows, cache)
-    T, dev = _slots(slots), slots.device
+    T, dev, form = _slots(slots), slots.device, _cache_format(format)
     parts, n_slots = b"", None
     for x, c in zip(rows, caches):
-        held, shape, n = _cache_part(c, format, dev)
+        held, shape, n = _cache_part(c, form, dev)
         if x.dtype is not torch.bfloat16 or x.shape != (T, *shape) or x.get_device() != dev.index:
             raise ValueError(f"rows must be bfloat16 {[T, *shape]} on {dev}, got {x.dtype} {list(x.shape)} on {x.device}")
         if n != n_slots and n_slots is not None:
             raise ValueError(f"the caches have {n_slots} and {n} slots")
         n_slots = n
         parts += _PART.pack(x.data_ptr(), *_rows_of(x, shape), *held)
-    _launch("kv_cache_write", dev, _CACHE[format][0], parts, len(caches), T, slots.data_ptr(), n_slots)
+    _launch("kv_cache_write", dev, form[0], parts, len(caches), T, slots.data_ptr(), n_slots)
 
 
 def _cache_read(name, cache, T, format, out_dtype, out, dev, index):
     outs, caches, one = _pair(out, cache)
+    form = _cache_format(format)
     code, parts, n_slots, got = _out_code(out_dtype), b"", None, []
     for o, c in zip(outs, caches):
-        held, shape, n = _cache_part(c, format, dev)
+        held, shape, n = _cache_part(c, form, dev)
         if o is None:
             o = torch.empty((T, *shape), dtype=out_dtype, device=dev)
         else:
@@ -473,7 +479,7 @@ def _cache_read(name, cache, T, format, out_dtype, out, dev, index):
         n_slots = n
         parts += _PART.pack(o.data_ptr(), 0, math.prod(shape), *held)
         got.append(o)
-    _launch(name, dev, _CACHE[format][0], parts, len(caches), T, *index, n_slots, code)
+    _launch(name, dev, form[0], parts, len(caches), T, *index, n_slots, code)
     return got[0] if one else tuple(got)
 
 
