@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_common.hpp"
 #include "launch.hpp"
@@ -361,49 +362,55 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void matvec_tile_kernel(Matv
   // piece q at q ^ (r % 16); then W's rows eight at a time, 8 pieces of 32 k
   // each, in the order 0 8 1 9 .. of their 16, row n's piece q at q ^ (n % 8).
   // Rows in that order and places: every fragment read spreads over all banks.
-  constexpr int kXLoads = (8 * MT + WAVES - 1) / WAVES;
-  uint32_t xo[kXLoads];
+  // Waves below ROWS / 8 load W too, and one of x more where WAVES does not
+  // divide 8 MT.
+  constexpr int kMostX = (8 * MT + WAVES - 1) / WAVES, kLeastX = 8 * MT / WAVES;
+  static_assert(8 * MT % WAVES == 0 || 8 * MT % WAVES == ROWS / 8, "");
+  uint32_t xo[kMostX];
 #pragma unroll
-  for (int k = 0; k < kXLoads; ++k) {
+  for (int k = 0; k < kMostX; ++k) {
     const int r = 2 * (wave + k * WAVES) + (lane >> 5);
     xo[k] = (uint32_t)min(r, tokens - 1) * (uint32_t)(2 * p.K) + 16 * ((lane & 31) ^ (r & 15));
   }
   const int slot = 8 * (wave & 1) + (lane >> 3), row = 16 * (wave >> 1) + (slot >> 1) + 8 * (slot & 1);
   const uint32_t wo = (uint32_t)min(row, rows - 1) * (uint32_t)(p.K / 2) + 16 * ((lane & 7) ^ (row & 7));
-  const bool loads_w = wave < ROWS / 8;  // wave-uniform
-  auto issue = [&](int c, int stage) {
+  const int full = p.K / kTileK;
+  auto issue = [&](auto both, int c, int stage) {  // a whole chunk
     u32x4* st = lds + stage * kStage + 64 * wave;
-    if ((c + 1) * kTileK <= p.K) {
 #pragma unroll
-      for (int k = 0; k < kXLoads; ++k)
-        if (wave + k * WAVES < 8 * MT) dma16s(reinterpret_cast<f16x8*>(st + 64 * k * WAVES), xb + (size_t)c * (2 * kTileK), xo[k]);
-      if (loads_w) dma16s(reinterpret_cast<f16x8*>(st + kXChunks), wq + (size_t)c * (kTileK / 2), wo);
-    } else {
-      // pieces behind the row's end: the row's first one instead, their products
-      // are left out.  (An offset holds 16 times its piece: never negative.)
-      const uint32_t left = (uint32_t)(p.K - c * kTileK);
-#pragma unroll
-      for (int k = 0; k < kXLoads; ++k) {
-        if (wave + k * WAVES >= 8 * MT) break;  // wave-uniform
-        const uint32_t piece = (lane & 31) ^ ((2 * (wave + k * WAVES) + (lane >> 5)) & 15);
-        dma16s(reinterpret_cast<f16x8*>(st + 64 * k * WAVES), xb,
-               8 * piece < left ? xo[k] + (uint32_t)c * (2 * kTileK) : xo[k] - 16 * piece);
-      }
-      const uint32_t piece = (lane & 7) ^ (row & 7);
-      if (loads_w)
-        dma16s(reinterpret_cast<f16x8*>(st + kXChunks), wq,
-               32 * piece < left ? wo + (uint32_t)c * (kTileK / 2) : wo - 16 * piece);
+    for (int k = 0; k < (both ? kMostX : kLeastX); ++k)
+      dma16s(reinterpret_cast<f16x8*>(st + 64 * k * WAVES), xb + (size_t)c * (2 * kTileK), xo[k]);
+    if constexpr (both) dma16s(reinterpret_cast<f16x8*>(st + kXChunks), wq + (size_t)c * (kTileK / 2), wo);
+  };
+  auto issue_any = [&](auto both, int c, int stage) {
+    if (c < full) {
+      issue(both, c, stage);
+      return;
     }
+    // pieces behind the row's end: the row's first one instead, their products
+    // are left out.  (An offset holds 16 times its piece: never negative.)
+    u32x4* st = lds + stage * kStage + 64 * wave;
+    const uint32_t left = (uint32_t)(p.K - c * kTileK);
+#pragma unroll
+    for (int k = 0; k < (both ? kMostX : kLeastX); ++k) {
+      const uint32_t piece = (lane & 31) ^ ((2 * (wave + k * WAVES) + (lane >> 5)) & 15);
+      dma16s(reinterpret_cast<f16x8*>(st + 64 * k * WAVES), xb,
+             8 * piece < left ? xo[k] + (uint32_t)c * (2 * kTileK) : xo[k] - 16 * piece);
+    }
+    const uint32_t piece = (lane & 7) ^ (row & 7);
+    if constexpr (both)
+      dma16s(reinterpret_cast<f16x8*>(st + kXChunks), wq,
+             32 * piece < left ? wo + (uint32_t)c * (kTileK / 2) : wo - 16 * piece);
   };
   // the scales of chunks seg .. seg + kTileSeg: a wave takes rows in turn, its
   // lanes the steps of 128 k
-  const int total = (p.K + kMvStep - 1) / kMvStep, full = p.K / kMvStep, rest = (p.K - full * kMvStep) / 32;
+  const int total = (p.K + kMvStep - 1) / kMvStep, whole = p.K / kMvStep, rest = (p.K - whole * kMvStep) / 32;
   const int pitch = (min(total, 2 * kTileSeg) | 1) * kUnit<FMT>;
   auto stage_scales = [&](int seg) {
     const int i = 2 * seg + lane;
     if (i < total)
       stage_step<FMT, ROWS / WAVES>(ws + (size_t)i * (kMvStep / kBlock), wave, WAVES, rows, p.K / kBlock,
-                                         i < full ? 4 : rest, scales + lane * kUnit<FMT>, pitch);
+                                         i < whole ? 4 : rest, scales + lane * kUnit<FMT>, pitch);
   };
 
   f32x4 acc[MT][U];
@@ -442,10 +449,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void matvec_tile_kernel(Matv
       for (int t = 0; t < MT; ++t) a[j][t] = *reinterpret_cast<const u32x4*>(st + ao[j] + t * (16 * 16 * 32));
     }
   };
-  auto compute = [&](int c) {
+  auto compute = [&](auto whole, int blocks) {  // the chunk's number of blocks
 #pragma unroll
     for (int j = 0; j < JB; ++j) {
-      if (c * kTileK + 32 * (JB * ks + j) >= p.K) break;  // wave-uniform
+      if (!whole && JB * ks + j >= blocks) break;  // wave-uniform
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const float s = FMT == kNvfp4 ? __builtin_amdgcn_cvt_f32_fp8(sc[j][u], 0) : __uint_as_float(sc[j][u] << 23);
@@ -457,26 +464,52 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void matvec_tile_kernel(Matv
     }
   };
 
-  const int mine = (8 * MT - wave + WAVES - 1) / WAVES + loads_w;  // loads of this wave and a chunk
-  issue(0, 0);
-  if (chunks > 1) issue(1, 1);
-  stage_scales(0);
-  for (int c = 0, stage = 0; c < chunks; ++c) {
-    // chunk c has landed, c + 1 may be on its way
-    if (c + 1 == chunks) wait_vmcnt<0>();
-    else if (mine == kXLoads + 1) wait_vmcnt<kXLoads + 1>();
-    else if (mine == kXLoads) wait_vmcnt<kXLoads>();
-    else wait_vmcnt<kXLoads - 1>();
-    lds_barrier();  // for every wave, and every wave has read chunk c - 1
-    if (c && c % kTileSeg == 0) {
-      stage_scales(c);
-      lds_barrier();
+  // A copy of the loop for each of the two counts of loads, without a branch but
+  // its own: the checks of one loop for all took 2 us of 19 (64 tokens, N16384).
+  auto run = [&](auto both) {
+    constexpr int kLoads = both ? kMostX + 1 : kLeastX;  // of this wave and a chunk
+    issue_any(both, 0, 0);
+    if (chunks > 1) issue_any(both, 1, 1);
+    stage_scales(0);
+    int c = 0, stage = 0;
+    auto next = [&] {
+      ++c;
+      stage = stage == kTileStages - 1 ? 0 : stage + 1;
+    };
+    auto behind = [&] { return stage ? stage - 1 : kTileStages - 1; };  // chunk c + 2's stage, as c - 1's
+    for (int seg = 0; c + 2 < full; seg += kTileSeg) {
+      const int end = min(seg + kTileSeg, full - 2);
+      if (seg) {
+        lds_barrier();  // every wave has read the scales of chunk c - 1
+        stage_scales(seg);
+      }
+#pragma unroll 1
+      while (c < end) {
+        wait_vmcnt<kLoads>();  // chunk c has landed, c + 1 may be on its way
+        lds_barrier();         // for every wave, and every wave has read chunk c - 1
+        read(c, stage);
+        issue(both, c + 2, behind());
+        SCHED_FENCE();  // the loads go out before the reads are waited for
+        compute(std::true_type(), 8);
+        next();
+      }
     }
-    read(c, stage);
-    if (c + 2 < chunks) issue(c + 2, stage ? stage - 1 : kTileStages - 1);
-    compute(c);
-    stage = stage == kTileStages - 1 ? 0 : stage + 1;
-  }
+    while (c < chunks) {  // the same with every check, three chunks at most
+      if (c + 1 < chunks) wait_vmcnt<kLoads>();
+      else wait_vmcnt<0>();
+      lds_barrier();
+      if (c && c % kTileSeg == 0) {
+        stage_scales(c);
+        lds_barrier();
+      }
+      read(c, stage);
+      if (c + 2 < chunks) issue_any(both, c + 2, behind());
+      compute(std::false_type(), (p.K - c * kTileK) / 32);
+      next();
+    }
+  };
+  if (ROWS / 8 == WAVES || wave < ROWS / 8) run(std::true_type());
+  else run(std::false_type());
 
   // the waves of a row group add their sums
   constexpr int kTiles = ROWS / 16, kSums = MT * kTiles * 64;
