@@ -567,35 +567,36 @@ void launch_few(const MatvecParams& p, hipStream_t s) {
       <<<(unsigned)((p.N + 16 * NT - 1) / (16 * NT)), 64 * kFewWaves, lds, s>>>(p);
 }
 
-// Which kernel, by what was measured on both sides (us, K4096 and K7168).
-//   M <= 8: 16 rows per workgroup; NVFP4 with 32 (M <= 4) or 64 rows where these
-//   run at once and workgroups of 16 rows do not, three of which fit on a CU
-//   (M1: N16384 9.1 against 10.8, N12288 8.6 against 7.8, N18432 12.4 against
-//   11.6; M8: N16384 11.3 against 12.3, N12288 10.7 against 10.8, N8192 10.3
-//   against 7.3, N18432 18.9 against 14.8).
-//   M <= 16: 16 rows up to two workgroups per CU, then 32 (N8192 9.0 against
-//   9.5, N16384 16.6 against 13.3).
-//   Many rows of W: the tiles, whose x is read once per 64 rows (NVFP4 M8:
-//   N24576 K7168 28.0 against 29.5, N20480 27.2 against 20.5; M16: N20480 17.8
-//   against 18.1, N16384 13.6 against 13.3; MXFP4 M4: N28672 K7168 21.9 against
-//   27.3; NVFP4 M4 never).
+// Which kernel, by what was measured on both sides (us, K4096 unless it says).
+//   M <= 4: a few rows per workgroup, 16, or for NVFP4 32 where workgroups of 32
+//   run at once and those of 16 do not, three of which fit on a CU (M1: N16384
+//   9.1 against 10.8, N12288 8.6 against 7.8, N18432 12.4 against 11.6).  MXFP4
+//   with many rows takes the tiles (M4 K7168 N28672 21.9 against 27.3; NVFP4 never).
+//   M <= 8: 16 rows up to three workgroups per CU, for NVFP4 64 where these run
+//   at once and three of 16 do not (K7168: N16384 15.4 against 16.1 with the
+//   tiles, N20480 20.7 with the tiles against 21.8; MXFP4 N12288 11.0 against
+//   12.4, N14336 13.9 against 12.5).
+//   M <= 16: 16 rows up to two per CU (K2048 N8192 and N10240: NVFP4 6.2 and 8.4 against
+//   6.0 and 7.7 with the tiles, MXFP4 5.2 and 6.6 against 4.8 and 6.5; N4096 6.1 and 5.0 against 7.9 and 6.7).
+//   The tiles of up to 16 tokens: 32 rows where three per CU hold all of them
+//   (K7168: NVFP4 N24576 25.7 against 33.1 with 64 rows, N28672 36.3 against 28.9).
 template <int FMT>
 void launch_format(const MatvecParams& p, hipStream_t s) {
   const int64_t rows16 = (p.N + 15) / 16, rows32 = (p.N + 31) / 32, rows64 = (p.N + 63) / 64;
-  const bool rounds = rows16 > 3 * kCus;  // 16-row workgroups do not run all at once
+  const bool at_once = rows16 <= 3 * kCus;  // 16-row workgroups run all at once
   if (p.M <= 4 && (FMT == kNvfp4 || rows16 <= 7 * kCus)) {
     if constexpr (FMT == kMxfp4) launch_few<FMT, false, 1, 1, 8>(p, s);
-    else if (rounds && rows32 <= 2 * kCus) launch_few<FMT, true, 1, 2, 4>(p, s);
+    else if (!at_once && rows32 <= 2 * kCus) launch_few<FMT, true, 1, 2, 4>(p, s);
     else launch_few<FMT, true, 1, 1, 6>(p, s);
-  } else if (p.M <= 8 && rows16 <= 6 * kCus) {
+  } else if (p.M <= 8 && (at_once || (FMT == kNvfp4 && rows64 <= kCus))) {
     if constexpr (FMT == kMxfp4) launch_few<FMT, false, 2, 1, 6>(p, s);
-    else if (rounds && rows64 <= kCus) launch_few<FMT, true, 2, 4, 2>(p, s);
-    else launch_few<FMT, true, 2, 1, 4>(p, s);
-  } else if (p.M > 4 && p.M <= 16 && rows16 <= 4 * kCus) {
-    if (rows16 <= 2 * kCus) launch_few<FMT, false, 4, 1, 4>(p, s);
-    else launch_few<FMT, false, 4, 2, 4>(p, s);
+    else if (at_once) launch_few<FMT, true, 2, 1, 4>(p, s);
+    else launch_few<FMT, true, 2, 4, 2>(p, s);
+  } else if (p.M <= 16 && rows16 <= 2 * kCus) {
+    launch_few<FMT, false, 4, 1, 4>(p, s);
   } else if (p.M <= 16) {
-    launch_tile<FMT, 1, 64, 8>(p, s);
+    if (rows32 <= 3 * kCus) launch_tile<FMT, 1, 32, 8>(p, s);
+    else launch_tile<FMT, 1, 64, 8>(p, s);
   } else if (p.M <= 32) {
     launch_tiles<FMT, 2>(p, s);
   } else if (p.M <= 48) {
