@@ -328,16 +328,16 @@ __global__ __launch_bounds__(64 * kFewWaves, OCC) void matvec_few_kernel(MatvecP
 // chunks ahead, and read from there by the wave that needs them: the waves
 // share the rows by 32 (or 16) and a chunk's eight blocks of 32 k.
 //
-// Bound by what a CU does per chunk rather than by memory (M64 K4096 N16384: 19.3 us NVFP4,
-// 15.6 MXFP4; loads alone 12.6 and 11.6, and the same without the loads in the
-// loop 17.3 and 13.2): a conversion and two multiplications per pair of NVFP4
-// weights beside the MFMAs, which share the issue slots of a SIMD (16 MFMAs
-// and 64 VALU instructions take about what both take by themselves), the
-// fragments' way out of LDS, a barrier.  Two waves per SIMD instead of four:
-// 20.6 and 16.6.  Measured and not kept: conversions spread between the MFMAs
-// by hand, fragments read a chunk ahead, x and W loaded by different waves with
-// W four chunks ahead (each 0 to 15 % slower); chunks in another order per
-// workgroup (3 % slower).
+// Bound by the streams into LDS and by what a CU does with them, each by itself
+// nearly as long as both (M64 K4096 N16384: 16.5 us NVFP4, 13.7 MXFP4; the loads
+// alone 13.1 and 12.4, everything but the loads 14.2 and 11.4): 32 KiB of x and 8
+// of W per chunk and CU; a conversion and two multiplications per pair of NVFP4
+// weights beside the MFMAs, which share the issue slots of a SIMD; the fragments'
+// way out of LDS, a barrier.  64 rows with two waves per SIMD instead of four:
+// 18.0 and 13.6.  Measured and not kept: fragments read a chunk ahead (NVFP4 16.4,
+// MXFP4 13.8 and more for fewer rows); conversions spread between the MFMAs by
+// hand, x and W loaded by different waves with W four chunks ahead, chunks in
+// another order per workgroup (0 to 15 % slower).
 constexpr int kTileK = 256, kTileStages = 3;
 constexpr int kTileSeg = 32;  // chunks whose scales are in LDS at a time
 
@@ -549,8 +549,10 @@ constexpr int64_t kCus = 256;
 
 // The smallest tile with which every workgroup has a CU of its own: all of them
 // read all of x, so more than one on a CU costs what a larger tile saves, and
-// with fewer rows a workgroup is done sooner (NVFP4 M64 K4096: N4096 11.4, 12.6 and
-// 17.6 us with 16, 32 and 64 rows, N8192 20.8, 13.0 and 17.8, N16384 39.6, 24.0 and 18.6).
+// with fewer rows a workgroup is done sooner (NVFP4 M64 K4096: N4096 10.2, 11.3 and
+// 14.4 us with 16, 32 and 64 rows, N8192 18.2, 12.0 and 14.9, N16384 32.8, 21.6
+// and 16.5; M32, of which two fit on a CU: N8192 10.3 with 16 rows and 9.2 with
+// 32, N16384 14.6 with 32 and 12.4 with 64).
 template <int FMT, int MT>
 void launch_tiles(const MatvecParams& p, hipStream_t s) {
   const int64_t slices = (p.M + 16 * MT - 1) / (16 * MT);
