@@ -437,7 +437,7 @@ def _slots(slots):
         raise ValueError(f"slots must be [T], got {list(slots.shape)}")
     if slots.dtype is not torch.int32 or not slots.is_cuda or not slots.is_contiguous():
         _require(slots, torch.int32, "slots")
-    return len(slots)
+    return slots.shape[0]
 
 
 def cache_write(rows, slots, cache, format="mxfp8"):

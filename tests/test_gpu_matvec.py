@@ -73,7 +73,9 @@ WIDE = [(1, 288, 12289), (3, 288, 16383), (2, 96, 16500), (4, 160, 28700), (6, 2
         (20, 288, 4097), (30, 352, 8200), (47, 288, 8191), (40, 160, 8193), (64, 480, 5000), (64, 288, 8200),
         (50, 544, 16390), (100, 288, 2100), (130, 32, 6000),
         (1, 17056, 40), (3, 33184, 33), (8, 17056, 18), (6, 20000, 66), (16, 17088, 20), (11, 32800, 5),
-        (20, 8352, 30), (40, 16800, 17), (64, 8320, 50), (33, 24672, 9), (1, 2 ** 20, 3), (64, 2 ** 20, 2)]
+        (20, 8352, 30), (40, 16800, 17), (64, 8320, 50), (33, 24672, 9), (1, 2 ** 20, 3), (64, 2 ** 20, 2),
+        (40, 512, 4200), (20, 768, 9000), (64, 256, 8300), (16, 768, 12000), (64, 8192, 40), (64, 8704, 70), (33, 8960, 40),
+        (14, 8448, 8300)]
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
