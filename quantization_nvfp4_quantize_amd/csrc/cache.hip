@@ -165,7 +165,7 @@ constexpr uint32_t kSkip = 0xfffffffeu;   // the row belongs to no sequence and 
 __device__ __forceinline__ uint32_t slot_of_row(const CacheParams& p, uint32_t t) {
   int lo = 0, hi = p.B;  // the first b with cu_lens[b + 1] > t
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
+    const int mid = lo + ((hi - lo) >> 1);  // lo + hi may pass 2^31
     if (p.cu_lens[mid + 1] > (int64_t)t) hi = mid;
     else lo = mid + 1;
   }

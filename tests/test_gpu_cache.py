@@ -216,6 +216,21 @@ def test_cache_read_pages_outside_the_table(nv):
     assert torch.equal(out, want)
 
 
+def test_cache_read_pages_of_many_sequences(nv):
+    """More than 2^30 sequences, nearly all of them empty: the search for a row's
+    sequence goes through indices whose sums pass 2^31."""
+    B, at = 2 ** 30 + 5, 2 ** 30 + 2
+    cache = nv.cache_empty(16, (32,), device="cuda:0")
+    nv.cache_write(_rows(1, 16, (32,)).abs() + 1, torch.arange(16, dtype=torch.int32, device="cuda:0"), cache)
+    full = nv.cache_read(cache, torch.arange(16, dtype=torch.int32, device="cuda:0"))
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda:0")
+    cu[at + 1:], cu[B] = 1, 2
+    pages = torch.zeros(B, 1, dtype=torch.int32, device="cuda:0")
+    pages[at], pages[B - 1] = 3, 1
+    got = nv.cache_read_pages(cache, pages, cu, 4, 2)
+    assert torch.equal(got, full[[12, 4]])
+
+
 def test_cache_beyond_4_gib(nv):
     """4.6 GiB of elements: slots on both sides of 2^32 bytes."""
     shape, n = (8, 128), 4_800_000
