@@ -473,7 +473,9 @@ typedef struct {
  *   parts    one or two (keys and values), R may differ
  *   out      bf16 (out_dtype 0, rounded to nearest even) or fp32 (1, for the MX
  *            formats exact): e2m1 * sf * gs as nvfp4_dequantize, element *
- *            2^(c - 127)
+ *            2^(c - 127).  Format 2: a product of 2^128 or more, to which
+ *            values from 1.9375 * 2^127 on are rounded, is read as bf16's
+ *            largest value (255/128 * 2^127): finite rows come back finite
  *   slots    int32 [T];  pages int32 [B][pages_per_seq];  cu_lens int32
  *            [B + 1], rising.  All on the device.
  * T is the number of rows of the inputs or outputs; R <= 2^20 and (T + 1) * R

@@ -157,6 +157,7 @@ __device__ __forceinline__ f32x2 pair_fp8(uint32_t q, int h) {
   return h ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q, 1.0f, true) : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q, 1.0f, false);
 }
 
+constexpr float kLargestBf16 = 0x1.fep127f;
 constexpr uint32_t kZeros = 0xffffffffu;  // the row is read as zeros
 constexpr uint32_t kSkip = 0xfffffffeu;   // the row belongs to no sequence and is left as it was
 
@@ -246,6 +247,14 @@ __global__ __launch_bounds__(kCacheThreads) void cache_read_kernel(CacheParams p
       const int e = (int)code[u] - 127;
 #pragma unroll
       for (int k = 0; k < kUnit; ++k) v[k] = ldexpf(v[k], e);
+      // Blocks with a maximum above 1.75 * 2^127 have code 247, and elements from
+      // 1.9375 * 2^127 on are rounded up to 2^128 there.  They stand for bf16
+      // values, so they are read as the largest of these.  (NaN stays.)
+      if (FMT == kMxfp8 && code[u] >= 247) {
+#pragma unroll
+        for (int k = 0; k < kUnit; ++k)
+          if (isinf(v[k])) v[k] = copysignf(kLargestBf16, v[k]);
+      }
     }
     u32x4 o;
     if constexpr (BF16_OUT) {

@@ -136,6 +136,34 @@ def test_mxfp8_every_bf16_value(nv):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_mxfp8_largest_values_come_back_finite(nv, dtype):
+    """The bf16 values whose blocks have the largest code a write makes, 247: the
+    elements that are rounded up to 2^128 are read as bf16's largest value, all
+    within half a step, 2^-4; then every element byte under every code from there on."""
+    top = np.arange(0x7f00, 0x7f80, dtype=np.uint16)
+    x = np.zeros((2 * len(top), 32), np.uint16)
+    x[:, 0] = np.concatenate([top, top | 0x8000])
+    x[:, 1:] = np.resize(np.concatenate([top[::-1], np.arange(0, 0x7f80, 0x155, dtype=np.uint16)]), (len(x), 31))
+    x[:, 1:] = np.minimum(x[:, 1:], x[:, :1] & 0x7fff) | (np.arange(31) % 2 << 15).astype(np.uint16)
+    d = dev_bf16(x)
+    cache = nv.cache_empty(len(x), (32,), device="cuda:0")
+    at = torch.arange(len(x), dtype=torch.int32, device="cuda:0")
+    nv.cache_write(d, at, cache)
+    assert int(cache[1].max()) == 247
+    largest = 255 / 128 * 2.0 ** 127
+    got = nv.cache_read(cache, at, out_dtype=dtype).double().cpu().numpy()
+    assert np.array_equal(got, np.clip(values(host(cache[0]), host(cache[1]), "mxfp8"), -largest, largest))
+    xd = d.double().cpu().numpy()
+    assert (np.abs(got - xd) <= np.maximum(np.abs(xd) * 2.0 ** -4, 2.0 ** 120 * 2.0 ** -10)).all()
+    codes = np.arange(247, 255)
+    q = np.tile(np.arange(256, dtype=np.uint8), (len(codes), 1))
+    s = np.repeat(codes.astype(np.uint8)[:, None], 8, axis=1)
+    cache = torch.from_numpy(q).to("cuda:0"), torch.from_numpy(s).to("cuda:0")
+    got = nv.cache_read(cache, at[:len(codes)], out_dtype=dtype).double().cpu().numpy()
+    assert np.array_equal(got, np.clip(values(q, s, "mxfp8"), -largest, largest), equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 def test_cache_read_every_byte(nv, dtype):
     """Every element byte under every scale byte of each format (values inside
     fp32; bf16 rounds to nearest even)."""
