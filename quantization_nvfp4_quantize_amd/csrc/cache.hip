@@ -54,7 +54,7 @@ struct PartParams {
 struct CacheParams {
   PartParams part[2];
   const int32_t* slots;  // nullable: by page table
-  uint32_t n_slots, T;
+  uint32_t n_slots;
   const int32_t* pages;    // [B][wide]
   const int32_t* cu_lens;  // [B + 1]
   int B, wide, page_size;
@@ -276,7 +276,6 @@ CacheParams params_of(const CachePart* parts, int n, int64_t T) {
     const uint32_t r8 = (uint32_t)(s.R / 8);
     p.part[i] = {s.x, s.x_stride, s.out, s.q, s.s, s.gs, r8, (uint32_t)(T * r8), fast_div(r8)};
   }
-  p.T = (uint32_t)T;
   return p;
 }
 
