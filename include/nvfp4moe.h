@@ -463,6 +463,8 @@ typedef struct {
  * kv_cache_write -- row t of every part goes to slot slots[t].  Slots outside
  * [0, n_slots) are skipped (a padded batch), other slots are left as they
  * were.  A slot that occurs twice in one call holds unspecified bytes after.
+ * An infinite or NaN value leaves the bytes of its own block unspecified, in
+ * whatever format; other blocks and rows keep theirs.
  * kv_cache_read -- row t of every output is what slot slots[t] holds, zeros
  * where that is outside [0, n_slots).
  * kv_cache_read_pages -- the same by page table: rows cu_lens[b] ..

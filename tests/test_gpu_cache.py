@@ -288,6 +288,24 @@ def test_cache_skipped_rows_may_hold_anything(nv):
         assert not cache[0][[1, 2, 5, 6, 7]].any() and not cache[1][[1, 2, 5, 6, 7]].any()
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_cache_infinite_and_nan_values_stay_in_their_block(nv, fmt):
+    T, shape, block = 9, (3, 96), BLOCK[fmt]
+    gs = _gs(fmt)
+    x, at = _rows(8, T, shape), torch.arange(T, dtype=torch.int32, device="cuda:0")
+    caches = [nv.cache_empty(T, shape, fmt, "cuda:0", gs) for _ in range(2)]
+    nv.cache_write(x, at, caches[0], format=fmt)
+    hit = torch.zeros(T, 3, 96 // block, dtype=torch.bool, device="cuda:0")
+    for t, h, k, v in ((0, 0, 0, float("inf")), (2, 1, 50, float("nan")), (2, 2, 95, -float("inf")), (8, 2, 31, float("nan")),
+                       (5, 0, 32, float("inf")), (5, 0, 33, float("nan"))):
+        x[t, h, k] = v
+        hit[t, h, k // block] = True
+    nv.cache_write(x, at, caches[1], format=fmt)
+    for a, b in zip(caches[0][:2], caches[1][:2]):
+        a, b = (c.unflatten(-1, (96 // block, -1))[~hit] for c in (a, b))
+        assert torch.equal(a, b)
+
+
 def test_cache_streams_and_graphs(nv):
     """Written and read on a stream of its own, and captured: every replay
     writes and reads what the inputs hold then, padding included."""
