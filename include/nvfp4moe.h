@@ -429,7 +429,9 @@ int mxfp4_linear(const uint16_t *x, int64_t M, int64_t K, const uint8_t *w_q, co
  *   per 64 tokens, which for many tokens is slower than the linears' tiles.
  *   x, w_q and out 16-byte, the scales 4-byte aligned.  A token with infinite
  *   or NaN values gets results that are not finite, the others keep theirs.
- *   No workspace.
+ *   w_gs multiplies the finished sum: results are finite where the terms'
+ *   magnitudes without it add up to less than 2^128 (a token of 1e35 under
+ *   scales next to 448 may pass that, whatever w_gs is).  No workspace.
  */
 int nvfp4_matvec(const uint16_t *x, int64_t M, int64_t K, const uint8_t *w_q, const uint8_t *w_sf,
                  const float *w_gs, int64_t N, int out_dtype, void *out, void *stream);

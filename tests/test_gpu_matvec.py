@@ -253,6 +253,22 @@ def test_matvec_largest_and_smallest_values(nv, fmt, M):
         assert (np.abs(got - ref) <= (K + 2) * (2.0 ** -24 * mag + 2.0 ** -149)).all()
 
 
+@pytest.mark.parametrize("M", [1, 7, 16, 40])
+@pytest.mark.parametrize("top,gs", [(106, 2.0 ** -100), (106, 2.0 ** -1), (-100, 2.0 ** 100)])
+def test_matvec_tensor_scale_on_large_and_small_sums(nv, M, top, gs):
+    """The tensor scale multiplies the finished sum: magnitudes up to 2^128 before it are right after it."""
+    rng = np.random.Generator(np.random.PCG64(M))
+    K, N = 1184, 50
+    q, _ = weights(rng, N, K, "nvfp4")
+    s = rng.integers(0x70, 0x7f, (N, K // 16), dtype=np.uint8)  # 128 to 448
+    x = torch.from_numpy(rng.uniform(-1, 1, (M, K))).bfloat16().double().numpy() * 2.0 ** top
+    w = values(q, s, "nvfp4")
+    ref, mag = x @ w.T, np.abs(x) @ np.abs(w).T
+    assert mag.max() < 2.0 ** 128 and (top < 0 or mag.max() > 2.0 ** 124)
+    got = nv.matvec(torch.from_numpy(x).bfloat16().to("cuda:0"), _dev(q), _dev(s), _gs(gs), out_dtype=torch.float32)
+    _check(got, ref * gs, mag * gs, K, torch.float32)
+
+
 def test_matvec_two_graphs_on_two_streams(nv):
     """Two captured calls of each kernel, replayed side by side: nothing is shared."""
     rng = np.random.Generator(np.random.PCG64(14))
