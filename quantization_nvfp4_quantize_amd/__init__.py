@@ -345,6 +345,7 @@ def matvec(x, w_q, w_sf, w_gs, out_dtype=torch.bfloat16, out=None):
     """Products of a few tokens with NVFP4 weights, the activations kept in bf16:
     y [M][N] = x @ deq(W)^T (bf16 or float32).  x bf16 [M][K], K % 32 == 0; w_q
     [N][K/2], w_sf [N][K/16], w_gs float32 [1] as linear takes them, any N.
+    out: a tensor to fill, whose type then counts (as in linear).
     Made for M up to 64 (the weights are read once per 64 tokens)."""
     return _matvec("nvfp4_matvec", x, w_q, w_sf, w_gs, 16, out_dtype, out)
 
@@ -486,7 +487,8 @@ def _cache_read(name, cache, T, format, out_dtype, out, dev, index):
 def cache_read(cache, slots, format="mxfp8", out_dtype=torch.bfloat16, out=None):
     """Rows of a cache, dequantized: [T][*row_shape] (bf16 or float32) with row t
     from slot slots[t] (int32 [T]), zeros where that is outside the cache.  For
-    two caches (keys and values) a pair.  out: tensor(s) to fill, of out_dtype."""
+    two caches (keys and values) a pair.  out: tensor(s) to fill, of out_dtype
+    (one of another type is refused)."""
     T = _slots(slots)
     return _cache_read("kv_cache_read", cache, T, format, out_dtype, out, slots.device, (slots.data_ptr(),))
 

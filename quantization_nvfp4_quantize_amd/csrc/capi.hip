@@ -512,8 +512,8 @@ int mxfp4_linear(const uint16_t* x, int64_t M, int64_t K, const uint8_t* w_q, co
 // ------------------------------------------------------------------ few tokens, 4-bit weights
 namespace {
 
-// T and N of a call of few tokens: grid.y counts slices of tokens, and the
-// kernels keep K in 32 bits.
+// M, K and N of a call of few tokens: grid.y counts slices of tokens, and the
+// kernels keep K, and offsets within 64 rows of x or of W, in 32 bits.
 constexpr int64_t kMaxMatvecDim = (int64_t)1 << 20;
 
 int matvec(const char* name, int fmt, const uint16_t* x, int64_t M, int64_t K, const uint8_t* w_q, const uint8_t* w_s,
@@ -560,8 +560,7 @@ struct CacheCall {
 };
 
 // The checks that the three calls share, and the parts as the launchers take
-// them.  rows: the bf16 input of a write, the output of a read (out_bytes per
-// element).
+// them.  rows: the bf16 input of a write, the output of a read.
 int cache_parts(const char* name, int format, const kv_cache_part* parts, int n_parts, int64_t T, int64_t n_slots,
                 bool write, CacheCall* c) {
   g_last_error[0] = 0;
