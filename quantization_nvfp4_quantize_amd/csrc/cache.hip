@@ -7,8 +7,9 @@
 // into chunks of 8 elements: a lane loads 16 bytes of bf16, the 2 (NVFP4) or 4
 // (MX) lanes of a block exchange their maxima with DPP, and a block never
 // straddles two rows because R is a multiple of its length.  Both directions are
-// bound by memory: 5.9 TB/s written into MXFP8 (T16384, keys and values), 6.0
-// read back (a copy of 2 + 2 GiB moves 4.9), with streaming stores for what the
+// bound by memory: writing MXFP8 (T16384, keys and values) moves 5.9 TB/s, reading
+// 24 sequences 6.0 with the cache's bytes partly in the memory-side cache and 4.9
+// without, what a copy of 2 + 2 GiB moves; with streaming stores for what the
 // call does not read again.
 #include <hip/hip_runtime.h>
 
@@ -294,6 +295,11 @@ void read_with(const CacheParams& p, int n, hipStream_t s) {
 // Four units per thread keep enough loads in flight for large reads (24 sequences
 // of up to 8192 rows of 576: 28.5 us against 38.6 with one, 29.6 with two); where
 // that leaves CUs without a workgroup, one (262 rows of 8 x 128, keys and values: 3.35 us against 4.1).
+// Rows of 576 by slot into bf16, one unit against four (us, NVFP4 and MXFP8), at
+// workgroups of four units: 120 2.60 and 3.33, 2.58 and 3.36; 250 2.97 and 3.53,
+// 3.01 and 3.52; 500 3.38 and 3.74, 3.64 and 4.02; 700 4.36 and 4.26, 4.85 and 4.51;
+// 2000 9.44 and 9.36, 10.61 and 10.10.  One would do better up to some 600; the
+// bound stands where every CU has work.
 template <int FMT, bool BF16_OUT>
 void read_as(const CacheParams& p, int n, hipStream_t s) {
   const dim3 g = grid_of(p, n, BF16_OUT ? 8 : 4, 4 * kCacheThreads);

@@ -552,7 +552,9 @@ constexpr int64_t kCus = 256;
 // with fewer rows a workgroup is done sooner (NVFP4 M64 K4096: N4096 10.2, 11.3 and
 // 14.4 us with 16, 32 and 64 rows, N8192 18.2, 12.0 and 14.9, N16384 32.8, 21.6
 // and 16.5; M32, of which two fit on a CU: N8192 10.3 with 16 rows and 9.2 with
-// 32, N16384 14.6 with 32 and 12.4 with 64).
+// 32, N16384 14.6 with 32 and 12.4 with 64).  Beyond N16384 there is a second
+// round, a mostly empty one at first (M64 K4096: N18432 28.0 us, N28672 29.3; MXFP4
+// 23.9 and 25.2).
 template <int FMT, int MT>
 void launch_tiles(const MatvecParams& p, hipStream_t s) {
   const int64_t slices = (p.M + 16 * MT - 1) / (16 * MT);
@@ -578,8 +580,14 @@ void launch_few(const MatvecParams& p, hipStream_t s) {
 //   at once and three of 16 do not (K7168: N16384 15.4 against 16.1 with the
 //   tiles, N20480 20.7 with the tiles against 21.8; MXFP4 N12288 11.0 against
 //   12.4, N14336 13.9 against 12.5).
-//   M <= 16: 16 rows up to two per CU (K2048 N8192 and N10240: NVFP4 6.2 and 8.4 against
-//   6.0 and 7.7 with the tiles, MXFP4 5.2 and 6.6 against 4.8 and 6.5; N4096 6.1 and 5.0 against 7.9 and 6.7).
+//   M <= 16: 16 rows up to two per CU.  N4096 is clear (6.1 against 8.0 with the
+//   tiles, MXFP4 5.2 against 6.7), and so is N10240 (11.2 against 10.9, MXFP4 10.1
+//   against 9.0).  Between, with W from HBM, where a decode step finds it, N8192:
+//   NVFP4 M9 9.3 against 9.7, M16 10.1 against 9.9; MXFP4 8.3 against 9.0 and 9.4
+//   against 9.2; K7168 NVFP4 13.2 against 14.1 and 15.2 against 14.2, MXFP4 12.4
+//   against 13.2 and 14.4 against 13.4; K2048 6.8 against 6.8 and 7.3 against 6.9,
+//   MXFP4 5.9 against 6.2 and 6.5 against 6.3.  With W in the memory-side cache
+//   the tiles are ahead by 1 to 2 %, MXFP4 by 2 to 9 %.
 //   The tiles of up to 16 tokens: 32 rows where three per CU hold all of them
 //   (K7168: NVFP4 N24576 25.7 against 33.1 with 64 rows, N28672 36.3 against 28.9).
 template <int FMT>
